@@ -14,7 +14,7 @@ call raises.
 """
 from .api import (  # noqa: F401
     FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_MISALIGNED,
-    FA_ERR_CUDA, FA_ERR_TIMEOUT, FaError, library, library_path,
+    FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_INDEX, FaError, library, library_path,
     fa_fwd, fa_bwd, fa_bwd_workspace_size, fa_get_device_error, fa_strerror,
     fa_bwd_preprocess, fa_bwd_main, fa_bwd_dq_convert,
     fa_bwd_noalloc, FA_BWD_NOALLOC_MAX_WORKSPACE_BYTES, fa_selftest_wait_timeout,
@@ -24,4 +24,6 @@ from .api import (  # noqa: F401
     attention_forward, attention_backward, attention_decode, attention_forward_qk8,
     attention_forward_fp8,
     attention_forward_bias, attention_backward_bias,
+    fa_rope_table, fa_qk_norm_rope, fa_qk_norm_rope_bwd, fa_qk_norm_rope_bwd_workspace_size,
+    fa_paged_append, rope_table, qk_norm_rope, qk_norm_rope_backward, paged_append,
 )

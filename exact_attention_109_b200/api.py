@@ -18,6 +18,7 @@ FA_ERR_UNSUPPORTED = 2
 FA_ERR_MISALIGNED = 3
 FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
+FA_ERR_INDEX = 6
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libfa_sm100.so"
@@ -87,6 +88,20 @@ def library():
     lib.fa_bwd_bias.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i,
                                 f, vp, sz, vp]
     lib.fa_bwd_bias.restype = i
+    lp, db = ctypes.POINTER(ll), ctypes.c_double
+    lib.fa_rope_table.argtypes = [vp, ll, i, db, vp]
+    lib.fa_rope_table.restype = i
+    lib.fa_qk_norm_rope.argtypes = [vp, vp, vp, lp, vp, vp, i, f, vp, ll, i, i, vp, vp, vp, vp,
+                                    i, i, i, i, i, vp]
+    lib.fa_qk_norm_rope.restype = i
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, vp, lp, vp, vp, i, f, vp, ll, i, i, vp,
+                                        vp, vp, vp, lp, vp, vp, i, i, i, i, i, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_paged_append.argtypes = [vp, vp, vp, lp, vp, vp, i, f, vp, ll, i, i, i, vp, vp, vp,
+                                    vp, vp, vp, i, i, i, i, i, i, i, i, vp]
+    lib.fa_paged_append.restype = i
     lib.fa_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
     lib.fa_selftest_wait_timeout.restype = i
     lib.fa_get_device_error.argtypes = [vp]
@@ -237,6 +252,61 @@ def fa_bwd_main_accumulate(q: int, k: int, v: int, dO: int, dk_acc: int, dv_acc:
 
 def fa_convert_f32_bf16(src: int, dst: int, n: int, stream: int = 0) -> int:
     return library().fa_convert_f32_bf16(src, dst, int(n), stream or None)
+
+
+def fa_rope_table(table: int, rows: int, rope_dim: int, base: float, stream: int = 0) -> int:
+    """Raw C call: fill the (cos, sin) table of `rows` positions."""
+    return library().fa_rope_table(table, int(rows), rope_dim, float(base), stream or None)
+
+
+def _longs(values):
+    return (ctypes.c_longlong * len(values))(*values) if values is not None else None
+
+
+def fa_qk_norm_rope(q: int, k: int, v: int, strides, q_weight: int, k_weight: int,
+                    weight_f32: int, eps: float, rope: int, rope_rows: int, rope_dim: int,
+                    interleaved: int, positions: int, q_out: int, k_out: int, v_out: int, B: int,
+                    N: int, Hq: int, Hkv: int, d: int, stream: int = 0) -> int:
+    """Raw C call: norm and rotation in front of attention; `strides` is a
+    sequence of nine element strides."""
+    return library().fa_qk_norm_rope(q, k, v or None, _longs(strides), q_weight or None,
+                                     k_weight or None, weight_f32, eps, rope or None, rope_rows,
+                                     rope_dim, interleaved, positions or None, q_out, k_out,
+                                     v_out or None, B, N, Hq, Hkv, d, stream or None)
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d: int) -> int:
+    return int(library().fa_qk_norm_rope_bwd_workspace_size(d))
+
+
+def fa_qk_norm_rope_bwd(dq_out: int, dk_out: int, dv_out: int, q: int, k: int, strides,
+                        q_weight: int, k_weight: int, weight_f32: int, eps: float, rope: int,
+                        rope_rows: int, rope_dim: int, interleaved: int, positions: int, dq: int,
+                        dk: int, dv: int, grad_strides, dq_weight: int, dk_weight: int, B: int,
+                        N: int, Hq: int, Hkv: int, d: int, workspace: int, workspace_bytes: int,
+                        stream: int = 0) -> int:
+    """Raw C call: the gradients of fa_qk_norm_rope; `strides` (six) and
+    `grad_strides` (nine) are sequences of element strides."""
+    return library().fa_qk_norm_rope_bwd(
+        dq_out, dk_out, dv_out or None, q or None, k or None, _longs(strides), q_weight or None,
+        k_weight or None, weight_f32, eps, rope or None, rope_rows, rope_dim, interleaved,
+        positions or None, dq, dk, dv or None, _longs(grad_strides), dq_weight or None,
+        dk_weight or None, B, N, Hq, Hkv, d, workspace or None, workspace_bytes, stream or None)
+
+
+def fa_paged_append(q: int, k: int, v: int, strides, q_weight: int, k_weight: int,
+                    weight_f32: int, eps: float, rope: int, rope_rows: int, rope_dim: int,
+                    interleaved: int, pos_offset: int, seq_start: int, cache_len: int,
+                    block_table: int, q_out: int, k_pages: int, v_pages: int, S: int, T: int,
+                    Hq: int, Hkv: int, d: int, page_size: int, num_pages: int, max_pages: int,
+                    stream: int = 0) -> int:
+    """Raw C call: append packed tokens to a paged cache; `strides` is a
+    sequence of six element strides."""
+    return library().fa_paged_append(
+        q, k, v, _longs(strides), q_weight or None, k_weight or None, weight_f32, eps,
+        rope or None, rope_rows, rope_dim, interleaved, pos_offset, seq_start, cache_len,
+        block_table, q_out, k_pages, v_pages, S, T, Hq, Hkv, d, page_size, num_pages, max_pages,
+        stream or None)
 
 
 def fa_selftest_wait_timeout(limit_us: int, stream: int = 0) -> int:
@@ -426,3 +496,251 @@ def attention_backward_bias(q, k, v, bias, out, lse, dO, causal: bool, scale: fl
                        B, H, N, d, bb, bh_, int(causal), scale, _ptr(workspace),
                        workspace.numel() * workspace.element_size(), s), "fa_bwd_bias")
     return dq, dk, dv, dbias
+
+
+# ------------------------------------------------ before attention, paged cache
+
+def _rows(name, t, shape, device):
+    """Element strides of a bf16 tensor whose last dimension is contiguous
+    (a dimension of one element gets stride 0)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return [s if n > 1 else 0 for s, n in zip(st[:-1], shape[:-1])]
+
+
+def _exact_tensor(name, t, shape, dtype, device):
+    """Data pointer of a contiguous tensor of exactly this shape and type."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _require_cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.device
+
+
+def _norm_rope_args(q_weight, k_weight, rope, d, device):
+    """(q_weight, k_weight, is fp32, table, its rows, its width) for the C calls."""
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight: give both or neither")
+    wq = wk = w32 = 0
+    if q_weight is not None:
+        if q_weight.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"q_weight: expected bfloat16 or float32, got {q_weight.dtype}")
+        wq = _exact_tensor("q_weight", q_weight, (d,), q_weight.dtype, device)
+        wk = _exact_tensor("k_weight", k_weight, (d,), q_weight.dtype, device)
+        w32 = int(q_weight.dtype == torch.float32)
+    if rope is None:
+        return wq, wk, w32, 0, 0, 0
+    if rope.dim() != 3 or rope.shape[2] != 2:
+        raise ValueError("rope: expected a [positions, rope_dim / 2, 2] table")
+    table = _exact_tensor("rope", rope, rope.shape, torch.float32, device)
+    return wq, wk, w32, table, rope.shape[0], 2 * rope.shape[1]
+
+
+class _Place:
+    """Makes a call's device current and, with a stream of the caller's,
+    allocates on it; `.raw` is the stream's handle."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+        self.raw = (stream or torch.cuda.current_stream(device)).cuda_stream
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cuda", stream=None):
+    """[positions, rope_dim / 2, 2] fp32 (cos, sin) of p * base^(-2i / rope_dim)."""
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("device: expected a CUDA device")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _Place(device, stream) as s:
+        table = torch.empty((max(0, int(positions)), max(0, rope_dim) // 2, 2),
+                            dtype=torch.float32, device=device)
+        _check(fa_rope_table(table.data_ptr(), positions, rope_dim, base, s), "fa_rope_table")
+    return table
+
+
+def qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-6, rope=None,
+                 positions=None, interleaved: bool = False, q_out=None, k_out=None, v_out=None,
+                 stream=None):
+    """q_out [B,Hq,N,d], k_out [B,Hkv,N,d] and v_out (None without v) =
+    fa_qk_norm_rope for CUDA bf16 q [B,N,Hq,d] and k, v [B,N,Hkv,d], of any
+    strides with the last dimension contiguous (such as parts of one
+    projection): RMS norm of each row with the weights (both or neither, bf16
+    or fp32) and rotation by the table ``rope`` (see ``rope_table``) at
+    ``positions`` [B,N] int32 (default: 0 .. N-1)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("expected [B, N, H, d] tensors")
+    device = _require_cuda("q", q)
+    B, N, Hq, d = q.shape
+    Hkv = k.shape[2]
+    strides = _rows("q", q, q.shape, device) + _rows("k", k, (B, N, Hkv, d), device)
+    if v is not None:
+        strides += _rows("v", v, (B, N, Hkv, d), device)
+    elif v_out is not None:
+        raise ValueError("v_out without v")
+    wq, wk, w32, table, rows, width = _norm_rope_args(q_weight, k_weight, rope, d, device)
+    pos = 0
+    if positions is not None:
+        pos = _exact_tensor("positions", positions, (B, N), torch.int32, device)
+    with _Place(device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, d), dtype=q.dtype, device=device)
+        if k_out is None:
+            k_out = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=device)
+        if v is not None and v_out is None:
+            v_out = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=device)
+        _check(fa_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), v.data_ptr() if v is not None else 0, strides, wq, wk,
+            w32, eps, table, rows, width, int(interleaved), pos,
+            _exact_tensor("q_out", q_out, (B, Hq, N, d), torch.bfloat16, device),
+            _exact_tensor("k_out", k_out, (B, Hkv, N, d), torch.bfloat16, device),
+            _exact_tensor("v_out", v_out, (B, Hkv, N, d), torch.bfloat16, device)
+            if v is not None else 0, B, N, Hq, Hkv, d, s), "fa_qk_norm_rope")
+    return q_out, k_out, v_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, dv_out, q, k, q_weight=None, k_weight=None,
+                          eps: float = 1e-6, rope=None, positions=None,
+                          interleaved: bool = False, dq=None, dk=None, dv=None, workspace=None,
+                          stream=None):
+    """dq, dk, dv, dq_weight, dk_weight = fa_qk_norm_rope_bwd: the gradients of
+    ``qk_norm_rope`` for upstream gradients dq_out [B,Hq,N,d], dk_out, dv_out
+    [B,Hkv,N,d] (dv_out None: no v).  dq, dk, dv are [B,N,H,d] bf16 of any
+    strides whose rows do not overlap (such as parts of one packed gradient;
+    default: contiguous); the weights' gradients are [d] fp32, None without
+    weights (q and k are then not read and may be None)."""
+    if dq_out.dim() != 4 or dk_out.dim() != 4:
+        raise ValueError("expected [B, H, N, d] gradients")
+    device = _require_cuda("dq_out", dq_out)
+    B, Hq, N, d = dq_out.shape
+    Hkv = dk_out.shape[1]
+    qs, ks = (B, N, Hq, d), (B, N, Hkv, d)
+    gq = _exact_tensor("dq_out", dq_out, (B, Hq, N, d), torch.bfloat16, device)
+    gk = _exact_tensor("dk_out", dk_out, (B, Hkv, N, d), torch.bfloat16, device)
+    gv = 0
+    if dv_out is not None:
+        gv = _exact_tensor("dv_out", dv_out, (B, Hkv, N, d), torch.bfloat16, device)
+    elif dv is not None:
+        raise ValueError("dv without dv_out")
+    wq, wk, w32, table, rows, width = _norm_rope_args(q_weight, k_weight, rope, d, device)
+    strides = None
+    if wq:
+        if q is None or k is None:
+            raise ValueError("q and k are needed for the gradients of a norm")
+        strides = _rows("q", q, qs, device) + _rows("k", k, ks, device)
+    pos = 0
+    if positions is not None:
+        pos = _exact_tensor("positions", positions, (B, N), torch.int32, device)
+    with _Place(device, stream) as s:
+        if dq is None:
+            dq = torch.empty(qs, dtype=torch.bfloat16, device=device)
+        if dk is None:
+            dk = torch.empty(ks, dtype=torch.bfloat16, device=device)
+        if dv is None and dv_out is not None:
+            dv = torch.empty(ks, dtype=torch.bfloat16, device=device)
+        grads = _rows("dq", dq, qs, device) + _rows("dk", dk, ks, device)
+        if dv is not None:
+            grads += _rows("dv", dv, ks, device)
+        dwq = dwk = None
+        if wq:
+            dwq = torch.empty(d, dtype=torch.float32, device=device)
+            dwk = torch.empty(d, dtype=torch.float32, device=device)
+            if workspace is None:
+                workspace = torch.empty(max(1, fa_qk_norm_rope_bwd_workspace_size(d)),
+                                        dtype=torch.uint8, device=device)
+        ws, ws_bytes = _workspace(workspace, device)
+        _check(fa_qk_norm_rope_bwd(
+            gq, gk, gv, q.data_ptr() if wq else 0, k.data_ptr() if wq else 0, strides, wq, wk,
+            w32, eps, table, rows, width, int(interleaved), pos, dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr() if dv is not None else 0, grads, dwq.data_ptr() if wq else 0,
+            dwk.data_ptr() if wq else 0, B, N, Hq, Hkv, d, ws, ws_bytes, s),
+            "fa_qk_norm_rope_bwd")
+    return dq, dk, dv, dwq, dwk
+
+
+def _workspace(workspace, device):
+    """(pointer, bytes) of a workspace tensor, (0, 0) without one."""
+    if workspace is None:
+        return 0, 0
+    if workspace.device != device:
+        raise ValueError(f"workspace: expected device {device}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _cache_shape(k_pages, device):
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages: expected [num_pages, Hkv, page_size, d]")
+    return tuple(k_pages.shape)
+
+
+def paged_append(q, k, v, k_pages, v_pages, block_table, seq_start, cache_len, rope=None,
+                 pos_offset: int = 0, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, stream=None):
+    """q_out [T,Hq,d] = fa_paged_append: the T packed new tokens q [T,Hq,d] and
+    k, v [T,Hkv,d] (CUDA bf16, any strides with the last dimension contiguous)
+    of S sequences go behind their ``cache_len`` [S] rows in k_pages, v_pages
+    [num_pages, Hkv, page_size, d], found through ``block_table``
+    [S, max_pages], normed and turned as in ``qk_norm_rope`` at position
+    pos_offset + key index.  ``seq_start`` [S+1] holds each sequence's first
+    token; all three are int32.  Rows of q_out that belong to no sequence are
+    not written."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("expected [T, H, d] tensors")
+    device = _require_cuda("q", q)
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    strides = _rows("q", q, q.shape, device) + _rows("k", k, (T, Hkv, d), device) \
+        + _rows("v", v, (T, Hkv, d), device)
+    pages, heads, page_size, _ = shape = _cache_shape(k_pages, device)
+    if heads != Hkv:
+        raise ValueError(f"k_pages: expected {Hkv} heads, got {heads}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [S, max_pages]")
+    S, max_pages = block_table.shape
+    kp = _exact_tensor("k_pages", k_pages, (pages, Hkv, page_size, d), torch.bfloat16, device)
+    vp = _exact_tensor("v_pages", v_pages, shape, torch.bfloat16, device)
+    bt = _exact_tensor("block_table", block_table, (S, max_pages), torch.int32, device)
+    ss = _exact_tensor("seq_start", seq_start, (S + 1,), torch.int32, device)
+    cl = _exact_tensor("cache_len", cache_len, (S,), torch.int32, device)
+    wq, wk, w32, table, rows, width = _norm_rope_args(q_weight, k_weight, rope, d, device)
+    with _Place(device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
+        qo = _exact_tensor("q_out", q_out, (T, Hq, d), torch.bfloat16, device)
+        if T:
+            _check(fa_paged_append(
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, wq, wk, w32, eps, table, rows,
+                width, int(interleaved), pos_offset, ss, cl, bt, qo, kp, vp, S, T, Hq, Hkv, d,
+                page_size, pages, max_pages, s), "fa_paged_append")
+    return q_out

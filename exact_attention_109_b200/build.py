@@ -8,14 +8,16 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "fa_api.cu"),
-           os.path.join(HERE, "csrc", "fa_noalloc.cu")]
+           os.path.join(HERE, "csrc", "fa_noalloc.cu"),
+           os.path.join(HERE, "csrc", "fa_rope.cu")]
 
 
 def headers():
-    """Every header the sources can include: all of csrc/*.cuh and include/*.h."""
+    """Every header the sources can include: all of csrc/*.cuh, csrc/*.h and include/*.h."""
     out = []
-    for folder, ext in ((os.path.join(HERE, "csrc"), ".cuh"), (os.path.join(ROOT, "include"), ".h")):
-        out += sorted(os.path.join(folder, f) for f in os.listdir(folder) if f.endswith(ext))
+    for folder in (os.path.join(HERE, "csrc"), os.path.join(ROOT, "include")):
+        out += sorted(os.path.join(folder, f) for f in os.listdir(folder)
+                      if f.endswith((".cuh", ".h")))
     return out
 
 OUT = os.path.join(HERE, "libfa_sm100.so")

@@ -17,6 +17,7 @@
 #include "fa_fwd1_kernel.cuh"
 #include "fa_fwd64_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
+#include "fa_internal.h"
 #include "fa_merge_kernels.cuh"
 
 // Set (bitwise OR) by a kernel whose pipeline wait ran out; one per device.
@@ -332,6 +333,24 @@ fa::FwdParams fwd_params(float* lse, unsigned int* err, int N, long long bh, int
 
 }  // namespace
 
+namespace fa_host {
+
+fa_status device(int* dev, unsigned int** err_word, int* sm_count) {
+    const fa_status st = device_setup(dev, err_word);
+    if (st == FA_OK) *sm_count = g_dev[*dev].sm_count;
+    return st;
+}
+
+bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, int cols, long long rows,
+                long long planes, int box_cols, int box_rows) {
+    if (!load_encode()) return false;
+    const CUtensorMapDataType t = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return encode_3d(map, base, t, elem_bytes, cols, rows, planes, box_cols, box_rows);
+}
+
+}  // namespace fa_host
+
 extern "C" {
 
 const char* fa_strerror(fa_status s) {
@@ -342,6 +361,7 @@ const char* fa_strerror(fa_status s) {
         case FA_ERR_MISALIGNED: return "FA_ERR_MISALIGNED: pointer not 16-byte aligned";
         case FA_ERR_CUDA: return "FA_ERR_CUDA: CUDA call failed";
         case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: device pipeline wait ran out";
+        case FA_ERR_INDEX: return "FA_ERR_INDEX: page, length or position out of range";
     }
     return "unknown fa_status";
 }
@@ -821,6 +841,7 @@ fa_status fa_get_device_error(void* stream) {
     if (word != 0 && cudaMemcpyToSymbol(g_fa_error_word, &zero, sizeof(zero)) != cudaSuccess)
         return FA_ERR_CUDA;
     if (word & fa::kErrTimeout) return FA_ERR_TIMEOUT;
+    if (word == fa::kErrIndex) return FA_ERR_INDEX;
     return word ? FA_ERR_CUDA : FA_OK;
 }
 

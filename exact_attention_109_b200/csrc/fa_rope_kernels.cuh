@@ -1,0 +1,518 @@
+// fa_rope_kernels.cuh -- what stands between a projection and attention: the
+// RMS norm of every head's query and key row, the position rotation, and the
+// move from the projection's token-major rows into the layout the attention
+// kernels read ([B, H, N, d], or the pages of a cache), in one pass.
+//
+// Forward, per row x of d values:  rstd = (mean(x^2) + eps)^(-1/2),
+// u = x * rstd * w, and every pair (a, b) of u's first rope_dim values turned
+// by its angle: (a cos - b sin, b cos + a sin).  The pairs are (i, i + rope/2)
+// or, interleaved, (2i, 2i + 1).
+// Backward, with g the upstream gradient turned back by the same angles:
+//   dw = sum over rows of g * x * rstd
+//   dx = rstd * (g w - x rstd * mean(g w x rstd)).
+//
+// These passes are bound by HBM: 2 bytes read and 2 written per value against
+// about ten fp32 operations.  So a row is held in registers by d / 8 lanes
+// (one 16-byte access each; 16 rows of 128 or 32 of 64 per CTA), its sums go
+// through shuffles, and everything that depends on the token alone (sequence,
+// page, angles) is read once and used for all heads the CTA walks.  All
+// arithmetic is fp32, rounded once on the way out.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+
+namespace fa {
+
+// Rows of one tensor: element strides of the batch (or nothing, for packed
+// tokens), the token and the head; the d values of a row are contiguous.
+struct HeadRows {
+    const __nv_bfloat16* p;
+    long long sb, sn, sh;
+};
+struct HeadRowsOut {
+    __nv_bfloat16* p;
+    long long sb, sn, sh;
+};
+
+struct RopeParams {
+    const float2* table;   // [rows][rope_dim / 2] (cos, sin), or null
+    long long rows;
+    int rope_dim;          // a multiple of 16; 0 without a table
+    const int* positions;  // [B][N], or null: token n has position n
+    const void* wq;        // [d], or null: no norm
+    const void* wk;
+    int w_f32;             // the weights are fp32 (else bf16)
+    float eps;
+    int B, N, Hq, Hkv;
+    int heads_per_cta;
+    unsigned int* err;
+};
+
+// Where a paged cache takes the tokens (PAGED).
+struct PagedDest {
+    const int* seq_start;    // [S + 1]
+    const int* cache_len;    // [S]
+    const int* block_table;  // [S][max_pages]
+    int S, max_pages, page_shift, num_pages, pos_offset;
+    __nv_bfloat16* q_out;    // [T][Hq][d]
+    __nv_bfloat16* k_pages;  // [num_pages][Hkv][page][d]
+    __nv_bfloat16* v_pages;
+};
+
+struct PrepOut {
+    __nv_bfloat16 *q, *k, *v;  // [B][H][N][d]; v may be null
+};
+
+constexpr int kRopeThreads = 256;
+
+__device__ __forceinline__ uint4 ld_row16(const __nv_bfloat16* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+}
+
+__device__ __forceinline__ float weight_at(const void* w, int f32, int i) {
+    return f32 ? static_cast<const float*>(w)[i]
+               : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
+}
+
+// Sum over the LANES (8 or 16) lanes that share a row.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// One lane's share of the rotation: it holds values [8c, 8c + 8) of a row.
+template <int D, bool INTERLEAVED>
+struct Turn {
+    static constexpr int LANES = D / 8;
+    bool on;        // these values are turned
+    int src;        // lane that holds the other members of the pairs
+    int other;      // index of the pair partner of value 8c (INTERLEAVED: unused)
+    float sign;     // -1: this lane holds the pairs' first members
+    float c[8], s[8];
+
+    // c and s of every value, from the token's row of the table.
+    __device__ __forceinline__ void load(const RopeParams& p, long long pos, int lane) {
+        const int col = lane & (LANES - 1), e0 = 8 * col;
+        on = e0 < p.rope_dim;
+        src = lane;
+        other = e0;
+        sign = -1.f;
+        if (!on) return;
+        const float4* row =
+            reinterpret_cast<const float4*>(p.table + pos * (p.rope_dim / 2));
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // two pairs per 16 bytes
+                const float4 f = __ldg(row + 2 * col + i);
+                c[4 * i] = c[4 * i + 1] = f.x;
+                s[4 * i] = s[4 * i + 1] = f.y;
+                c[4 * i + 2] = c[4 * i + 3] = f.z;
+                s[4 * i + 2] = s[4 * i + 3] = f.w;
+            }
+        } else {
+            const int half = p.rope_dim / 2;
+            const bool second = e0 >= half;
+            sign = second ? 1.f : -1.f;
+            other = second ? e0 - half : e0 + half;
+            src = (lane & ~(LANES - 1)) | (other >> 3);
+            const int i0 = second ? e0 - half : e0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = __ldg(row + i0 / 2 + i);
+                c[2 * i] = f.x;
+                s[2 * i] = f.y;
+                c[2 * i + 1] = f.z;
+                s[2 * i + 1] = f.w;
+            }
+        }
+    }
+
+    __device__ __forceinline__ float sign_of(int j) const {
+        return INTERLEAVED ? ((j & 1) ? 1.f : -1.f) : sign;
+    }
+    __device__ __forceinline__ int partner_index(int e0, int j) const {
+        return INTERLEAVED ? (e0 + (j ^ 1)) : (other + j);
+    }
+    // The pair partners of the eight values in `w` (all lanes take part).
+    __device__ __forceinline__ void partners(const uint4& w, const float (&x)[8],
+                                             float (&y)[8]) const {
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+        } else {
+            uint4 t;
+            t.x = __shfl_sync(0xffffffffu, w.x, src);
+            t.y = __shfl_sync(0xffffffffu, w.y, src);
+            t.z = __shfl_sync(0xffffffffu, w.z, src);
+            t.w = __shfl_sync(0xffffffffu, w.w, src);
+            widen8(t, y);
+        }
+    }
+};
+
+// The position of a token, checked against the table; a bad one is reported
+// and read as 0.
+__device__ __forceinline__ long long checked_position(const RopeParams& p, long long pos,
+                                                      bool active) {
+    if (!p.table) return 0;
+    if (pos >= 0 && pos < p.rows) return pos;
+    if (active) atomicOr(p.err, kErrIndex);
+    return 0;
+}
+
+// The sequence of packed token t: the last s with seq_start[s] <= t.  One
+// token per sequence is a decoding server's usual call, so s = t is tried
+// before the binary search.  The caller has checked that t lies below
+// seq_start[S].
+__device__ __forceinline__ int sequence_of(const int* seq_start, int S, int t) {
+    if (t < S && seq_start[t] <= t && t < seq_start[t + 1]) return t;
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seq_start[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Grid: x over blocks of 256 / (D / 8) tokens, y over groups of heads.  The
+// heads are the Hq query heads, then Hkv key heads, then (with v) Hkv value
+// heads, which are moved unchanged.
+template <int D, bool INTERLEAVED, bool PAGED>
+__global__ void __launch_bounds__(kRopeThreads)
+    fa_prep_kernel(const HeadRows q, const HeadRows k, const HeadRows v, const RopeParams p,
+                   const PrepOut out, const PagedDest dst) {
+    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, U = 4;
+    const int lane = threadIdx.x & 31;
+    const int col = threadIdx.x & (LANES - 1), e0 = 8 * col;
+    const long long total = static_cast<long long>(p.B) * p.N;
+    long long row = static_cast<long long>(blockIdx.x) * TOKENS + threadIdx.x / LANES;
+    bool active = row < total;
+    if (!active) row = total - 1;
+    const long long b = PAGED ? 0 : row / p.N;
+    const long long n = PAGED ? row : row - b * p.N;
+
+    long long pos;
+    long long page_row = -1;  // row of the token in its page, over all pages; -1: nowhere
+    long long page = 0;
+    if constexpr (PAGED) {
+        const int t = static_cast<int>(row);
+        if (t >= dst.seq_start[dst.S] || t < dst.seq_start[0]) active = false;  // no sequence's
+        pos = 0;
+        if (active) {
+            const int s = sequence_of(dst.seq_start, dst.S, t);
+            const int have = dst.cache_len[s];
+            const long long at = static_cast<long long>(have) + (t - dst.seq_start[s]);
+            const long long slot = at >> dst.page_shift;
+            pos = at + dst.pos_offset;
+            if (have >= 0 && slot < dst.max_pages) {
+                page = dst.block_table[static_cast<long long>(s) * dst.max_pages + slot];
+                if (page >= 0 && page < dst.num_pages) page_row = at - (slot << dst.page_shift);
+            }
+            if (page_row < 0) atomicOr(p.err, kErrIndex);
+        }
+    } else {
+        pos = p.positions ? p.positions[row] : n;
+    }
+    Turn<D, INTERLEAVED> turn;
+    turn.load(p, checked_position(p, pos, active), lane);
+
+    const int heads = p.Hq + p.Hkv + (v.p ? p.Hkv : 0);
+    const int h0 = blockIdx.y * p.heads_per_cta;
+    const int h1 = min(h0 + p.heads_per_cta, heads);
+    const bool norm = p.wq != nullptr;
+
+#pragma unroll 1
+    for (int part = 0; part < 3; ++part) {  // queries, keys, values
+        const int first = part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv;
+        const int count = part == 0 ? p.Hq : p.Hkv;
+        const int a = max(h0, first), z = min(h1, first + count);
+        if (a >= z) continue;
+        const HeadRows& in = part == 0 ? q : part == 1 ? k : v;
+        const __nv_bfloat16* src = in.p + b * in.sb + n * in.sn + (a - first) * in.sh + e0;
+        // Destination of head `a` and the step to the next head.
+        __nv_bfloat16* to;
+        long long step;
+        bool write = active;
+        if constexpr (PAGED) {
+            if (part == 0) {
+                to = dst.q_out + (row * p.Hq + a) * D + e0;
+                step = D;
+            } else {
+                write = page_row >= 0;
+                step = static_cast<long long>(D) << dst.page_shift;
+                to = (part == 1 ? dst.k_pages : dst.v_pages) +
+                     (page * p.Hkv + (a - first)) * step + (write ? page_row : 0) * D + e0;
+            }
+        } else {
+            step = static_cast<long long>(p.N) * D;
+            to = (part == 0 ? out.q : part == 1 ? out.k : out.v) +
+                 (b * count + (a - first)) * step + n * D + e0;
+        }
+        if (part == 2) {
+#pragma unroll 1
+            for (int h = a; h < z; h += U) {
+                uint4 w[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (h + u < z) w[u] = ld_row16(src + u * in.sh);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (h + u < z && write) *reinterpret_cast<uint4*>(to + u * step) = w[u];
+                src += U * in.sh;
+                to += U * step;
+            }
+            continue;
+        }
+        // y_j = rstd * (x_j * own_j + partner_j * cross_j)
+        float own[8], cross[8];
+        const void* wt = part == 0 ? p.wq : p.wk;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w0 = norm ? weight_at(wt, p.w_f32, e0 + j) : 1.f;
+            own[j] = turn.on ? w0 * turn.c[j] : w0;
+            cross[j] = 0.f;
+            if (turn.on) {
+                const float w1 =
+                    norm ? weight_at(wt, p.w_f32, turn.partner_index(e0, j)) : 1.f;
+                cross[j] = turn.sign_of(j) * w1 * turn.s[j];
+            }
+        }
+#pragma unroll 1
+        for (int h = a; h < z; h += U) {
+            uint4 w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                w[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (h + u < z) w[u] = ld_row16(src + u * in.sh);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[8], xp[8], y[8];
+                widen8(w[u], x);
+                turn.partners(w[u], x, xp);
+                float rstd = 1.f;
+                if (norm) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
+                    rstd = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + p.eps);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[j] = rstd * (turn.on ? fmaf(x[j], own[j], xp[j] * cross[j]) : x[j] * own[j]);
+                if (h + u < z && write) *reinterpret_cast<uint4*>(to + u * step) = narrow8(y);
+            }
+            src += U * in.sh;
+            to += U * step;
+        }
+    }
+}
+
+// Gradients of fa_prep_kernel's training form.  A CTA walks (token block, head
+// group) items; with a norm it leaves its sums of dw for queries and keys in
+// `part` [CTAs][2][D], which fa_dw_reduce_kernel adds up in a fixed order.
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads)
+    fa_prep_bwd_kernel(const HeadRows dyq, const HeadRows dyk, const HeadRows dyv,
+                       const HeadRows xq, const HeadRows xk, const HeadRowsOut dq,
+                       const HeadRowsOut dk, const HeadRowsOut dv, const RopeParams p,
+                       int token_blocks, int head_groups, float* part_dw) {
+    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, U = 2;
+    const int lane = threadIdx.x & 31;
+    const int col = threadIdx.x & (LANES - 1), e0 = 8 * col;
+    const long long total = static_cast<long long>(p.B) * p.N;
+    const int heads = p.Hq + p.Hkv + (dyv.p ? p.Hkv : 0);
+    const bool norm = p.wq != nullptr;
+    float dw[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
+
+    const long long items = static_cast<long long>(token_blocks) * head_groups;
+#pragma unroll 1
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const long long tb = it / head_groups;
+        const int h0 = static_cast<int>(it - tb * head_groups) * p.heads_per_cta;
+        const int h1 = min(h0 + p.heads_per_cta, heads);
+        long long row = tb * TOKENS + threadIdx.x / LANES;
+        const bool active = row < total;
+        if (!active) row = total - 1;
+        const long long b = row / p.N, n = row - b * p.N;
+        Turn<D, INTERLEAVED> turn;
+        turn.load(p, checked_position(p, p.positions ? p.positions[row] : n, active), lane);
+
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            const int first = part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv;
+            const int count = part == 0 ? p.Hq : p.Hkv;
+            const int a = max(h0, first), z = min(h1, first + count);
+            if (a >= z) continue;
+            const HeadRows& dy = part == 0 ? dyq : part == 1 ? dyk : dyv;
+            const HeadRowsOut& dx = part == 0 ? dq : part == 1 ? dk : dv;
+            const __nv_bfloat16* gsrc = dy.p + b * dy.sb + n * dy.sn + (a - first) * dy.sh + e0;
+            __nv_bfloat16* to = dx.p + b * dx.sb + n * dx.sn + (a - first) * dx.sh + e0;
+            if (part == 2) {
+#pragma unroll 1
+                for (int h = a; h < z; h += 4) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (h + u < z) w[u] = ld_row16(gsrc + u * dy.sh);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (h + u < z && active) *reinterpret_cast<uint4*>(to + u * dx.sh) = w[u];
+                    gsrc += 4 * dy.sh;
+                    to += 4 * dx.sh;
+                }
+                continue;
+            }
+            const HeadRows& xr = part == 0 ? xq : xk;
+            const __nv_bfloat16* xsrc =
+                norm ? xr.p + b * xr.sb + n * xr.sn + (a - first) * xr.sh + e0 : nullptr;
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = norm ? weight_at(part == 0 ? p.wq : p.wk, p.w_f32, e0 + j) : 1.f;
+#pragma unroll 1
+            for (int h = a; h < z; h += U) {
+                uint4 gr[U], xw[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    gr[u] = xw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (h + u < z) {
+                        gr[u] = ld_row16(gsrc + u * dy.sh);
+                        if (norm) xw[u] = ld_row16(xsrc + u * xr.sh);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float g[8], gp[8], y[8];
+                    widen8(gr[u], g);
+                    turn.partners(gr[u], g, gp);
+                    if (turn.on) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)  // the turn's transpose
+                            y[j] = fmaf(g[j], turn.c[j], -turn.sign_of(j) * gp[j] * turn.s[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) y[j] = g[j];
+                    }
+                    if (norm) {
+                        float x[8];
+                        widen8(xw[u], x);
+                        float ss = 0.f, gx = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            ss += x[j] * x[j];
+                            gx += y[j] * w[j] * x[j];
+                        }
+                        ss = row_sum<LANES>(ss);
+                        gx = row_sum<LANES>(gx);
+                        const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
+                        const float along = gx * rstd * (1.f / D);
+                        const bool mine = h + u < z && active;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float xh = x[j] * rstd;
+                            if (mine) dw[part == 0 ? 0 : 1][j] += y[j] * xh;
+                            y[j] = rstd * (y[j] * w[j] - xh * along);
+                        }
+                    }
+                    if (h + u < z && active)
+                        *reinterpret_cast<uint4*>(to + u * dx.sh) = narrow8(y);
+                }
+                gsrc += U * dy.sh;
+                xsrc += U * xr.sh;
+                to += U * dx.sh;
+            }
+        }
+    }
+    if (!norm) return;
+
+    // The CTA's sums: over the rows of each warp by shuffles, then over the
+    // warps through shared memory.
+    __shared__ float red[kRopeThreads / 32][2][D];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float x = dw[i][j];
+#pragma unroll
+            for (int o = LANES; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane < LANES) red[threadIdx.x >> 5][i][e0 + j] = x;
+        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * D; c += kRopeThreads) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRopeThreads / 32; ++w) x += red[w][c / D][c % D];
+        part_dw[static_cast<long long>(blockIdx.x) * 2 * D + c] = x;
+    }
+}
+
+// dw[c] = sum over `ctas` of part[cta][c]: 32 columns per CTA, 32 rows of
+// threads, always in the same order.
+template <int D>
+__global__ void __launch_bounds__(1024)
+    fa_dw_reduce_kernel(const float* part, int ctas, float* dwq, float* dwk) {
+    __shared__ float red[32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + x;
+    grid_dependency_wait();
+    float s = 0.f;
+#pragma unroll 8
+    for (int r = y; r < ctas; r += 32) s += part[static_cast<long long>(r) * 2 * D + c];
+    red[y][x] = s;
+    __syncthreads();
+    s = red[x][y];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (x == 0) {
+        const int col = blockIdx.x * 32 + y;
+        (col < D ? dwq : dwk)[col % D] = s;
+    }
+}
+
+// table[r][i] = (cos, sin) of r * base^(-2i / rope_dim), from 64-bit angles:
+// a position of 10^6 times a 32-bit frequency would be off by 0.06 rad.
+__global__ void fa_rope_table_kernel(float2* table, long long rows, int half, double base) {
+    const long long n = rows * half;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const long long r = i / half;
+        const double angle = static_cast<double>(r) *
+                             pow(base, -static_cast<double>(i - r * half) / half);
+        double s, c;
+        sincos(angle, &s, &c);
+        table[i] = make_float2(static_cast<float>(c), static_cast<float>(s));
+    }
+}
+
+}  // namespace fa

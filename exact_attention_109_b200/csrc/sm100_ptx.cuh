@@ -14,6 +14,7 @@ namespace fa {
 // Device error word values (read by fa_get_device_error).
 constexpr unsigned kErrTimeout = 1u;
 constexpr unsigned kErrLayout = 2u;  // shared-memory base not 1024-byte aligned
+constexpr unsigned kErrIndex = 4u;   // a page, length or position read from memory is out of range
 
 // Upper bound on any single pipeline wait, in nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

@@ -56,7 +56,9 @@ typedef enum {
     FA_ERR_UNSUPPORTED = 2,  /* d not in {64,128}, or no sm_100 device       */
     FA_ERR_MISALIGNED = 3,   /* a pointer is not 16-byte aligned             */
     FA_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed            */
-    FA_ERR_TIMEOUT = 5       /* a device-side pipeline wait ran out          */
+    FA_ERR_TIMEOUT = 5,      /* a device-side pipeline wait ran out          */
+    FA_ERR_INDEX = 6         /* a kernel read a page, length or position     */
+                             /* that is out of range (fa_get_device_error)   */
 } fa_status;
 
 /*
@@ -360,9 +362,123 @@ fa_status fa_decode_split_plan(int B, int H, int Nq, int Nk, int d,
                                int* qgroup_rows, int* n_splits, int* chunk);
 
 /*
+ * Between a projection and attention: the RMS norm of every head's query and
+ * key row, the rotation of positions, and the move from the projection's
+ * token-major rows to the layout the attention entry points read.
+ *
+ * For a row x of d values, with u = x * (mean(x^2) + eps)^(-1/2) * weight,
+ * every pair (a, b) among the first rope_dim values of u is turned by its
+ * angle: (a cos - b sin, b cos + a sin).  The pairs are (i, i + rope_dim/2),
+ * or (2i, 2i+1) with interleaved = 1.  The arithmetic is fp32, rounded once.
+ *
+ * Arguments that the three calls below share:
+ *   strides   HOST array of element strides of the inputs; the d values of a
+ *             row are contiguous.  Each stride is >= 0 (0 repeats a row) and
+ *             a multiple of 8.
+ *   q_weight, k_weight   [d] norm weights, fp32 if weight_f32 else bf16; both
+ *             NULL: no norm.  eps finite and > 0 (ignored without weights).
+ *   rope      [rope_rows][rope_dim / 2] (cos, sin) fp32 pairs, row p for
+ *             position p (as fa_rope_table writes them), or NULL: no
+ *             rotation.  rope_dim is a multiple of 16, 16 .. d; values beyond
+ *             it are not turned.
+ *   Hq is a multiple of Hkv, d in {64, 128}.  Inputs and outputs do not
+ *   overlap.  A position that the table does not hold is reported as
+ *   FA_ERR_INDEX by fa_get_device_error and its row's values are unspecified.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_MISALIGNED (rows and
+ * tables 16 bytes, int arrays 4, the workspace 256), FA_ERR_CUDA.
+ * (Not on the pages; RMS norm and rotary position embedding as published.)
+ *
+ * fa_rope_table -- table[p][i] = (cos, sin)(p * base^(-2i / rope_dim)) for
+ *   rows positions, from 64-bit angles.  rope_dim a multiple of 16 up to 128.
+ */
+fa_status fa_rope_table(float* table, long long rows, int rope_dim,
+                        double base, void* stream);
+
+/*
+ * fa_qk_norm_rope -- norm and rotation in front of fa_fwd.
+ *   q [B,N,Hq,d], k and v [B,N,Hkv,d] bf16 with strides[9] = (batch, token,
+ *             head) of q, k, v -- for example three parts of one projection.
+ *             v (with v_out) may be NULL; it is moved unchanged.
+ *   positions [B,N] int32, or NULL: token n has position n (rope_rows >= N).
+ *   q_out [B,Hq,N,d], k_out, v_out [B,Hkv,N,d] bf16, contiguous, written.
+ * One of the norm and the rotation may be absent, not both.  One launch.
+ */
+fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v,
+                          const long long* strides, const void* q_weight,
+                          const void* k_weight, int weight_f32, float eps,
+                          const float* rope, long long rope_rows, int rope_dim,
+                          int interleaved, const int* positions, void* q_out,
+                          void* k_out, void* v_out, int B, int N, int Hq,
+                          int Hkv, int d, void* stream);
+
+/*
+ * fa_qk_norm_rope_bwd -- its gradients, from those fa_bwd returns.
+ *   dq_out [B,Hq,N,d], dk_out, dv_out [B,Hkv,N,d] bf16, contiguous; dv_out
+ *             (with dv) may be NULL.
+ *   q, k, strides[6], weights, eps, rope, positions: as in the forward call;
+ *             q, k and strides are read only with weights.
+ *   dq, dk, dv  bf16 with grad_strides[9] (batch, token, head; HOST array),
+ *             overwritten; rows of one tensor do not overlap.  Parts of one
+ *             packed gradient are fine.
+ *   dq_weight, dk_weight [d] fp32, overwritten (with weights): summed over
+ *             batch, tokens and heads, bit for bit the same in every run.
+ *   workspace >= fa_qk_norm_rope_bwd_workspace_size(d) bytes, clobbered; may
+ *             be NULL without weights.
+ * One launch, and one more for the weights' gradients.
+ */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out,
+                              const void* dv_out, const void* q, const void* k,
+                              const long long* strides, const void* q_weight,
+                              const void* k_weight, int weight_f32, float eps,
+                              const float* rope, long long rope_rows,
+                              int rope_dim, int interleaved,
+                              const int* positions, void* dq, void* dk,
+                              void* dv, const long long* grad_strides,
+                              float* dq_weight, float* dk_weight, int B, int N,
+                              int Hq, int Hkv, int d, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * A paged key/value cache for a batch of S sequences.
+ *   k_pages, v_pages [num_pages, Hkv, page_size, d] bf16, contiguous;
+ *             page_size a power of two, 16 .. 256.
+ *   block_table [S, max_pages] int32: key j of sequence s is row j % page_size
+ *             of page block_table[s, j / page_size].
+ * New tokens are packed: T rows, those of sequence s being seq_start[s] ..
+ * seq_start[s+1]-1 (seq_start [S+1] int32, not decreasing, in 0 .. T).  A
+ * sequence may have none; rows outside seq_start[0] .. seq_start[S]-1 belong
+ * to nobody, and nothing is written for them.  Lengths, starts and pages are
+ * device memory and are read by the kernels, so a captured graph follows their
+ * values.  One that is out of range is reported as FA_ERR_INDEX by
+ * fa_get_device_error; nothing outside the given buffers is touched.
+ *
+ * fa_paged_append -- writes the new tokens' keys and values behind the rows
+ * that a sequence has, with norm and rotation on the way (see above).
+ *   q [T,Hq,d], k and v [T,Hkv,d] bf16 with strides[6] = (token, head) each.
+ *   cache_len [S] int32: rows each sequence had before; its i-th new token
+ *             becomes key cache_len[s] + i, at position pos_offset + that
+ *             (pos_offset >= 0: the length of a shared prefix).
+ *   q_out     [T,Hq,d] bf16, contiguous, written: the queries, turned.
+ * Norm and rotation may both be absent.  Two sequences must not share a page
+ * that the call writes.  T = 0 does nothing.  One launch.
+ */
+fa_status fa_paged_append(const void* q, const void* k, const void* v,
+                          const long long* strides, const void* q_weight,
+                          const void* k_weight, int weight_f32, float eps,
+                          const float* rope, long long rope_rows, int rope_dim,
+                          int interleaved, int pos_offset,
+                          const int* seq_start, const int* cache_len,
+                          const int* block_table, void* q_out, void* k_pages,
+                          void* v_pages, int S, int T, int Hq, int Hkv, int d,
+                          int page_size, int num_pages, int max_pages,
+                          void* stream);
+
+/*
  * fa_get_device_error -- synchronises `stream`, then reads and clears the
  * current device's error word.  Returns FA_ERR_TIMEOUT if a kernel's bounded
- * pipeline wait ran out since the last call, FA_ERR_CUDA if the stream
+ * pipeline wait ran out since the last call, FA_ERR_INDEX if a kernel met a
+ * page, length or position out of range, FA_ERR_CUDA if the stream
  * reports a CUDA error, FA_OK otherwise.
  * Cites: not on the pages (failure reporting of this library).
  */

@@ -26,4 +26,5 @@ from .api import (  # noqa: F401
     attention_forward_bias, attention_backward_bias,
     fa_rope_table, fa_qk_norm_rope, fa_qk_norm_rope_bwd, fa_qk_norm_rope_bwd_workspace_size,
     fa_paged_append, rope_table, qk_norm_rope, qk_norm_rope_backward, paged_append,
+    fa_fwd_paged, fa_paged_workspace_size, fa_paged_split_plan, attention_paged,
 )

@@ -102,6 +102,13 @@ def library():
     lib.fa_paged_append.argtypes = [vp, vp, vp, lp, vp, vp, i, f, vp, ll, i, i, i, vp, vp, vp,
                                     vp, vp, vp, i, i, i, i, i, i, i, i, vp]
     lib.fa_paged_append.restype = i
+    lib.fa_paged_workspace_size.argtypes = [i, i, i, i, i, i, i, i, i]
+    lib.fa_paged_workspace_size.restype = sz
+    lib.fa_paged_split_plan.argtypes = [i, i, i, i, i, i, i, i, i, i, ip, ip, ip]
+    lib.fa_paged_split_plan.restype = i
+    lib.fa_fwd_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i, i,
+                                 f, vp, sz, vp]
+    lib.fa_fwd_paged.restype = i
     lib.fa_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
     lib.fa_selftest_wait_timeout.restype = i
     lib.fa_get_device_error.argtypes = [vp]
@@ -307,6 +314,35 @@ def fa_paged_append(q: int, k: int, v: int, strides, q_weight: int, k_weight: in
         rope or None, rope_rows, rope_dim, interleaved, pos_offset, seq_start, cache_len,
         block_table, q_out, k_pages, v_pages, S, T, Hq, Hkv, d, page_size, num_pages, max_pages,
         stream or None)
+
+
+def fa_paged_workspace_size(S: int, T: int, Hq: int, Hkv: int, d: int, page_size: int,
+                            max_pages: int, prefix_len: int, max_new: int) -> int:
+    return int(library().fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
+                                                 prefix_len, max_new))
+
+
+def fa_paged_split_plan(S: int, T: int, Hq: int, Hkv: int, d: int, page_size: int,
+                        max_pages: int, prefix_len: int, max_new: int, sm_count: int):
+    """(status, prefix splits, keys per prefix split, own splits) of the host
+    split plan; pure host arithmetic, needs no GPU."""
+    ps, ch, os_ = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
+    st = library().fa_paged_split_plan(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len,
+                                       max_new, sm_count, ctypes.byref(ps), ctypes.byref(ch),
+                                       ctypes.byref(os_))
+    return st, ps.value, ch.value, os_.value
+
+
+def fa_fwd_paged(q: int, k_pages: int, v_pages: int, block_table: int, seq_start: int,
+                 kv_len: int, prefix_pages: int, prefix_len: int, o: int, lse: int, S: int,
+                 T: int, Hq: int, Hkv: int, d: int, page_size: int, num_pages: int,
+                 max_pages: int, max_new: int, scale: float, workspace: int,
+                 workspace_bytes: int, stream: int = 0) -> int:
+    """Raw C call: attention of packed new tokens over a paged cache."""
+    return library().fa_fwd_paged(q, k_pages, v_pages, block_table, seq_start, kv_len,
+                                  prefix_pages or None, prefix_len, o, lse, S, T, Hq, Hkv, d,
+                                  page_size, num_pages, max_pages, max_new, scale,
+                                  workspace or None, workspace_bytes, stream or None)
 
 
 def fa_selftest_wait_timeout(limit_us: int, stream: int = 0) -> int:
@@ -744,3 +780,59 @@ def paged_append(q, k, v, k_pages, v_pages, block_table, seq_start, cache_len, r
                 width, int(interleaved), pos_offset, ss, cl, bt, qo, kp, vp, S, T, Hq, Hkv, d,
                 page_size, pages, max_pages, s), "fa_paged_append")
     return q_out
+
+
+def attention_paged(q, k_pages, v_pages, block_table, seq_start, kv_len, scale: float,
+                    prefix_pages=None, prefix_len: int = 0, max_new: int | None = None, out=None,
+                    lse=None, workspace=None, stream=None):
+    """O [T,Hq,d], LSE [T,Hq] = fa_fwd_paged: the T packed new tokens q [T,Hq,d]
+    (CUDA bf16) of S sequences against the shared prefix -- the first
+    prefix_len keys of ``prefix_pages`` (int32) -- and their own ``kv_len`` [S]
+    keys (the new tokens' included, causal among them) in k_pages, v_pages
+    [num_pages, Hkv, page_size, d], found through ``block_table``
+    [S, max_pages].  ``seq_start`` [S+1] holds each sequence's first token; the
+    three are int32.  max_new: the most new tokens any sequence has (default:
+    T, which launches more work than a tight bound).  Rows that belong to no
+    sequence are not written."""
+    if q.dim() != 3:
+        raise ValueError("expected q [T, Hq, d]")
+    device = _require_cuda("q", q)
+    T, Hq, d = q.shape
+    qp = _exact_tensor("q", q, q.shape, torch.bfloat16, device)
+    pages, Hkv, page_size, _ = shape = _cache_shape(k_pages, device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [S, max_pages]")
+    S, max_pages = block_table.shape
+    kp = _exact_tensor("k_pages", k_pages, (pages, Hkv, page_size, d), torch.bfloat16, device)
+    vp = _exact_tensor("v_pages", v_pages, shape, torch.bfloat16, device)
+    bt = _exact_tensor("block_table", block_table, (S, max_pages), torch.int32, device)
+    ss = _exact_tensor("seq_start", seq_start, (S + 1,), torch.int32, device)
+    kl = _exact_tensor("kv_len", kv_len, (S,), torch.int32, device)
+    pp = 0
+    if prefix_len:
+        if prefix_pages is None:
+            raise ValueError("prefix_len without prefix_pages")
+        if page_size and prefix_pages.numel() * page_size < prefix_len:
+            raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages do not hold "
+                             f"{prefix_len} keys")
+        pp = _exact_tensor("prefix_pages", prefix_pages, (prefix_pages.numel(),), torch.int32,
+                           device)
+    most = T if max_new is None else int(max_new)
+    with _Place(device, stream) as s:
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+        op = _exact_tensor("out", out, (T, Hq, d), torch.bfloat16, device)
+        lp = _exact_tensor("lse", lse, (T, Hq), torch.float32, device)
+        if T:
+            if workspace is None:
+                need = fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
+                                               prefix_len, most)
+                if need:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            ws, ws_bytes = _workspace(workspace, device)
+            _check(fa_fwd_paged(qp, kp, vp, bt, ss, kl, pp, prefix_len, op, lp, S, T, Hq, Hkv, d,
+                                page_size, pages, max_pages, most, scale, ws, ws_bytes, s),
+                   "fa_fwd_paged")
+    return out, lse

@@ -9,6 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "fa_api.cu"),
            os.path.join(HERE, "csrc", "fa_noalloc.cu"),
+           os.path.join(HERE, "csrc", "fa_paged.cu"),
            os.path.join(HERE, "csrc", "fa_rope.cu")]
 
 

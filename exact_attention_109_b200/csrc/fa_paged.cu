@@ -1,0 +1,285 @@
+// fa_paged.cu -- C entry points of attention over a paged cache behind a
+// shared prefix (declared in include/fa.h; kernels in fa_paged_kernels.cuh).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "fa.h"
+#include "fa_internal.h"
+#include "fa_paged_kernels.cuh"
+
+namespace {
+
+using fa_host::aligned;
+
+constexpr int kMaxDevices = 64;
+// Work units (CTAs) that the splits aim at, at most: they bound the workspace.
+constexpr long long kMaxPrefixCtas = 512;
+constexpr long long kWantOwnCtas = 592;
+constexpr int kMaxOwnSplits = 256;
+
+struct Plan {
+    int tiles;            // query tiles per prefix CTA
+    int row_tiles;        // prefix CTAs along the rows
+    int prefix_splits, prefix_chunk;
+    int own_row_tiles, own_splits;
+};
+
+int ilog2(int x) {
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
+fa_status check_sizes(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages,
+                      int prefix_len, int max_new) {
+    if (S < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_pages < 1 || prefix_len < 0)
+        return FA_ERR_INVALID_ARG;
+    if (T > 0 && (max_new < 1 || max_new > T)) return FA_ERR_INVALID_ARG;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+        return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(T) * Hq > (1ll << 24) || prefix_len > (1 << 30) ||
+        static_cast<long long>(max_pages) * page_size > (1ll << 30))
+        return FA_ERR_INVALID_ARG;
+    // One CTA per sequence, 16-row tile, key head and split; 32-bit grid.
+    const long long tiles = (static_cast<long long>(max_new) * (Hq / Hkv) + 15) / 16;
+    if (T > 0 && static_cast<double>(S) * tiles * Hkv * kMaxOwnSplits > 2147483647.0)
+        return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+// Splits of the prefix: the fewest waves of CTAs (one per SM), a CTA's time
+// being its key blocks plus a fixed part of about three blocks' time (set-up,
+// the first loads, writing its partial result).
+void plan_prefix(Plan& pl, int T, int G, int Hkv, int prefix_len, int sm_count) {
+    pl.prefix_splits = 0;
+    pl.prefix_chunk = 0;
+    pl.row_tiles = 1;
+    pl.tiles = 1;
+    if (prefix_len == 0) return;
+    const long long rows = static_cast<long long>(T) * G;
+    pl.tiles = rows > 128 ? 2 : 1;
+    pl.row_tiles = static_cast<int>((rows + 128 * pl.tiles - 1) / (128 * pl.tiles));
+    const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
+    const long long blocks = (prefix_len + 127) / 128;
+    const long long most = std::min(blocks, std::max(1ll, kMaxPrefixCtas / units));
+    long long best = 0, best_cost = 0;
+    for (long long n = 1; n <= most; ++n) {
+        const long long per = (blocks + n - 1) / n;
+        if ((blocks + per - 1) / per != n) continue;  // the last split would be empty
+        const long long cost = ((units * n + sm_count - 1) / sm_count) * (per + 3);
+        if (best == 0 || cost < best_cost) {
+            best = n;
+            best_cost = cost;
+        }
+    }
+    pl.prefix_splits = static_cast<int>(best);
+    pl.prefix_chunk = static_cast<int>((blocks + best - 1) / best) * 128;
+}
+
+Plan make_plan(int S, int T, int Hq, int Hkv, int page_size, int max_pages, int prefix_len,
+               int max_new, int sm_count) {
+    Plan pl;
+    const int G = Hq / Hkv;
+    plan_prefix(pl, T, G, Hkv, prefix_len, sm_count);
+    pl.own_row_tiles = static_cast<int>((static_cast<long long>(max_new) * G + 15) / 16);
+    const long long units = static_cast<long long>(S) * pl.own_row_tiles * Hkv;
+    const long long cap = static_cast<long long>(max_pages) * page_size;
+    const long long most =
+        std::min<long long>(kMaxOwnSplits, (cap + fa::kOwnMinChunk - 1) / fa::kOwnMinChunk);
+    pl.own_splits = static_cast<int>(
+        std::max(1ll, std::min(most, (kWantOwnCtas + units - 1) / units)));
+    return pl;
+}
+
+// Opts the kernel into its shared memory and checks that the registers it is
+// launched with cover its setmaxnreg split.
+template <int D, int TILES>
+bool prepare_prefix() {
+    using T = fa::PrefixTraits<D, TILES>;
+    cudaFuncAttributes attr{};
+    return cudaFuncSetAttribute(fa::fa_prefix_kernel<D, TILES>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                T::SMEM_BYTES) == cudaSuccess &&
+           cudaFuncGetAttributes(&attr, fa::fa_prefix_kernel<D, TILES>) == cudaSuccess &&
+           attr.numRegs * T::NUM_THREADS >= T::REG_BUDGET;
+}
+template <int D>
+bool prepare_own() {
+    return cudaFuncSetAttribute(fa::fa_own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                fa::OwnTraits<D>::SMEM_BYTES) == cudaSuccess;
+}
+
+struct Ready {
+    std::once_flag once;
+    bool ok = false;
+};
+Ready g_ready[kMaxDevices];
+
+bool prepare(int dev) {
+    std::call_once(g_ready[dev].once, [&] {
+        g_ready[dev].ok = prepare_prefix<64, 1>() && prepare_prefix<64, 2>() &&
+                          prepare_prefix<128, 1>() && prepare_prefix<128, 2>() &&
+                          prepare_own<64>() && prepare_own<128>();
+    });
+    return g_ready[dev].ok;
+}
+
+template <class... Params, class... Args>
+cudaError_t launch(void (*kernel)(Params...), long long grid, int threads, size_t smem,
+                   bool overlap, cudaStream_t s, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <int D>
+cudaError_t launch_all(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv,
+                       const CUtensorMap& mp, const fa::PagedParams& prm, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    const bool prefix = pl.prefix_splits > 0;
+    if (prefix) {
+        const long long grid =
+            static_cast<long long>(prm.Hkv) * pl.row_tiles * pl.prefix_splits;
+        e = pl.tiles == 2
+                ? launch(fa::fa_prefix_kernel<D, 2>, grid, fa::PrefixTraits<D, 2>::NUM_THREADS,
+                         fa::PrefixTraits<D, 2>::SMEM_BYTES, false, s, mk, mv, mp, prm)
+                : launch(fa::fa_prefix_kernel<D, 1>, grid, fa::PrefixTraits<D, 1>::NUM_THREADS,
+                         fa::PrefixTraits<D, 1>::SMEM_BYTES, false, s, mk, mv, mp, prm);
+        if (e != cudaSuccess) return e;
+    }
+    const long long grid =
+        static_cast<long long>(prm.S) * pl.own_row_tiles * prm.Hkv * pl.own_splits;
+    e = launch(fa::fa_own_kernel<D>, grid, fa::OwnTraits<D>::THREADS,
+               fa::OwnTraits<D>::SMEM_BYTES, prefix, s, mk, mv, prm);
+    if (e != cudaSuccess || pl.prefix_splits + pl.own_splits == 1) return e;
+    const long long rows = static_cast<long long>(prm.T) * prm.Hq;
+    return launch(fa::fa_paged_merge_kernel<D>, (rows + 3) / 4, 128, 0, true, s, prm);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d, int page_size,
+                               int max_pages, int prefix_len, int max_new) {
+    if (check_sizes(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len, max_new) != FA_OK ||
+        T == 0)
+        return 0;
+    // Enough for any SM count: the splits are bounded by the sizes alone.
+    Plan pl = make_plan(S, T, Hq, Hkv, page_size, max_pages, prefix_len, max_new, 1);
+    long long slots = pl.own_splits;
+    if (prefix_len > 0) {
+        const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
+        slots += std::min<long long>((prefix_len + 127) / 128,
+                                     std::max(1ll, kMaxPrefixCtas / units));
+    }
+    return slots == 1 ? 0 : static_cast<size_t>(slots) * T * Hq * (d + 1) * sizeof(float);
+}
+
+fa_status fa_paged_split_plan(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages,
+                              int prefix_len, int max_new, int sm_count, int* prefix_splits,
+                              int* prefix_chunk, int* own_splits) {
+    if (!prefix_splits || !prefix_chunk || !own_splits || sm_count < 1) return FA_ERR_INVALID_ARG;
+    const fa_status st =
+        check_sizes(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len, max_new);
+    if (st != FA_OK) return st;
+    if (T == 0) return FA_ERR_INVALID_ARG;
+    const Plan pl =
+        make_plan(S, T, Hq, Hkv, page_size, max_pages, prefix_len, max_new, sm_count);
+    *prefix_splits = pl.prefix_splits;
+    *prefix_chunk = pl.prefix_chunk;
+    *own_splits = pl.own_splits;
+    return FA_OK;
+}
+
+fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                       const int* block_table, const int* seq_start, const int* kv_len,
+                       const int* prefix_pages, int prefix_len, void* o, float* lse, int S, int T,
+                       int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                       int max_new, float scale, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+    if (!q || !k_pages || !v_pages || !block_table || !seq_start || !kv_len || !o || !lse ||
+        (prefix_len > 0 && !prefix_pages))
+        return FA_ERR_INVALID_ARG;
+    if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+    const float sl2 = scale * 1.4426950408889634f;
+    if (!(std::isfinite(sl2) && sl2 > 0.f)) return FA_ERR_INVALID_ARG;
+    fa_status st = check_sizes(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len, max_new);
+    if (st != FA_OK) return st;
+    if (num_pages < 1 || static_cast<long long>(num_pages) * Hkv >= 0x7fffffffll)
+        return FA_ERR_INVALID_ARG;
+    const size_t need = fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
+                                                prefix_len, max_new);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
+        !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_start, 4) ||
+        !aligned(kv_len, 4) || !aligned(prefix_pages, 4) || !aligned(workspace, 256))
+        return FA_ERR_MISALIGNED;
+    if (T == 0) return FA_OK;
+    int dev, sms;
+    unsigned int* err;
+    if ((st = fa_host::device(&dev, &err, &sms)) != FA_OK) return st;
+    if (!prepare(dev)) return FA_ERR_CUDA;
+
+    const Plan pl = make_plan(S, T, Hq, Hkv, page_size, max_pages, prefix_len, max_new, sms);
+    const int slots = pl.prefix_splits + pl.own_splits;
+    fa::PagedParams prm;
+    prm.q = static_cast<const __nv_bfloat16*>(q);
+    prm.block_table = block_table;
+    prm.seq_start = seq_start;
+    prm.kv_len = kv_len;
+    prm.prefix_pages = prefix_pages;
+    prm.o = static_cast<__nv_bfloat16*>(o);
+    prm.lse = lse;
+    prm.part_o = static_cast<float*>(workspace);
+    prm.part_lse = workspace ? prm.part_o + static_cast<size_t>(slots) * T * Hq * d : nullptr;
+    prm.err = err;
+    prm.S = S;
+    prm.T = T;
+    prm.Hq = Hq;
+    prm.Hkv = Hkv;
+    prm.G = Hq / Hkv;
+    prm.R = T * prm.G;
+    prm.page_shift = ilog2(page_size);
+    prm.box_shift = std::min(prm.page_shift, 6);
+    prm.num_pages = num_pages;
+    prm.max_pages = max_pages;
+    prm.max_new = max_new;
+    prm.prefix_len = prefix_len;
+    prm.prefix_splits = pl.prefix_splits;
+    prm.prefix_chunk = pl.prefix_chunk;
+    prm.row_tiles = pl.row_tiles;
+    prm.own_splits = pl.own_splits;
+    prm.own_row_tiles = pl.own_row_tiles;
+    prm.scale_log2 = sl2;
+
+    const long long planes = static_cast<long long>(num_pages) * Hkv;
+    const int box = 1 << prm.box_shift;
+    CUtensorMap mk, mv, mp;
+    if (!fa_host::encode_map(&mk, k_pages, 2, d, page_size, planes, 64, box) ||
+        !fa_host::encode_map(&mv, v_pages, 2, d, page_size, planes, 64, box))
+        return FA_ERR_CUDA;
+    mp = mk;  // unused without a prefix
+    if (pl.prefix_splits > 0 &&
+        !fa_host::encode_map(&mp, prm.part_o, 4, d, prm.R,
+                             static_cast<long long>(pl.prefix_splits) * Hkv, 32, 32))
+        return FA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = d == 64 ? launch_all<64>(pl, mk, mv, mp, prm, s)
+                                  : launch_all<128>(pl, mk, mv, mp, prm, s);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

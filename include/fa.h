@@ -475,6 +475,52 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v,
                           void* stream);
 
 /*
+ * fa_fwd_paged -- attention of the packed new tokens over the paged cache,
+ * behind an optional prefix that all sequences share and that is read once
+ * for the whole batch (the split-KV merge of fa_fwd_decode joins the parts).
+ *   q         [T,Hq,d] bf16, contiguous.
+ *   kv_len    [S] int32: keys of each sequence, its new tokens included
+ *             (after fa_paged_append: cache_len + its new tokens).  With n
+ *             new tokens, its i-th sees the whole prefix and its own keys
+ *             j <= kv_len[s] - n + i.
+ *   prefix_pages [ceil(prefix_len / page_size)] int32 and prefix_len >= 0:
+ *             the shared prefix's pages, in order (NULL when prefix_len = 0).
+ *   max_new   the most new tokens any sequence has, 1 .. T; one with more is
+ *             reported as FA_ERR_INDEX and its rows are unspecified.
+ *   o         [T,Hq,d] bf16 and lse [T,Hq] fp32, written.  A row that sees no
+ *             key gets O = 0, LSE = -inf.
+ *   workspace >= fa_paged_workspace_size(...) bytes, 256-byte aligned,
+ *             clobbered; may be NULL when that is 0.
+ * Query head h reads key head h / (Hq / Hkv).  Cached rows that a token does
+ * not see may hold anything, infinities and NaN included, and never reach it.
+ * Weights are rounded to bf16 for P V and O is normalised by their sum, as in
+ * fa_fwd; scores, statistics and partial results are fp32.  Up to three
+ * launches.  Intended for a few new tokens per sequence; any number is right.
+ * T = 0 does nothing.  Limits: T * Hq <= 2^24, num_pages * Hkv < 2^31.
+ */
+size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d,
+                               int page_size, int max_pages, int prefix_len,
+                               int max_new);
+fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                       const int* block_table, const int* seq_start,
+                       const int* kv_len, const int* prefix_pages,
+                       int prefix_len, void* o, float* lse, int S, int T,
+                       int Hq, int Hkv, int d, int page_size, int num_pages,
+                       int max_pages, int max_new, float scale,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_paged_split_plan -- the work split fa_fwd_paged uses on a GPU with
+ * `sm_count` SMs: splits of the prefix (0: none) with prefix_chunk keys each
+ * (a multiple of 128), and splits of every sequence's own keys.  Host
+ * arithmetic only; touches no GPU.
+ */
+fa_status fa_paged_split_plan(int S, int T, int Hq, int Hkv, int d,
+                              int page_size, int max_pages, int prefix_len,
+                              int max_new, int sm_count, int* prefix_splits,
+                              int* prefix_chunk, int* own_splits);
+
+/*
  * fa_get_device_error -- synchronises `stream`, then reads and clears the
  * current device's error word.  Returns FA_ERR_TIMEOUT if a kernel's bounded
  * pipeline wait ran out since the last call, FA_ERR_INDEX if a kernel met a

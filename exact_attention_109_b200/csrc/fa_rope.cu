@@ -14,11 +14,13 @@ namespace {
 
 using fa_host::aligned;
 
-// CTAs of the backward kernel at most, and so rows of its dw partials: four
-// of 256 threads on each of 148 SMs.
-constexpr int kBwdCtas = 592;
+// CTAs of the backward kernel at most, and so rows of its dw partials: the two
+// that an SM's registers hold, on each of 148 SMs.
+constexpr int kBwdCtas = 296;
+constexpr long long kMinHeads = 2;  // heads that a CTA takes at least
 // CTAs below which the heads of a token block are spread over more CTAs.
 constexpr long long kWantCtas = 592;
+constexpr int kHeadsPerCta = 16;
 
 // Strides (in elements) of one input tensor: 16-byte rows, no negative step.
 bool strides_ok(const long long* s, int n) {
@@ -87,10 +89,13 @@ fa::RopeParams rope_params(const void* wq, const void* wk, int w_f32, float eps,
     return p;
 }
 
-// Groups the heads are cut into when `blocks` token blocks alone leave SMs
-// idle.
+// Groups the heads are cut into: enough CTAs to fill the SMs, and no more
+// than about 16 heads for one.  16384 tokens of 48 heads of 128: 73 us with all
+// heads in a CTA, 69.5 with 24, 68 with 16 (the last wave is shorter), 77 with
+// 10 (the set-up of a CTA counts).
 int head_groups(long long blocks, int heads) {
-    const long long g = (kWantCtas + blocks - 1) / blocks;
+    const long long g =
+        std::max<long long>((kWantCtas + blocks - 1) / blocks, heads / kHeadsPerCta);
     return static_cast<int>(std::max(1ll, std::min<long long>(g, heads)));
 }
 
@@ -126,12 +131,11 @@ cudaError_t launch_prep_bwd(const fa::HeadRows (&dy)[3], const fa::HeadRows (&x)
     constexpr int TOKENS = fa::kRopeThreads / (D / 8);
     const long long blocks = (static_cast<long long>(p.B) * p.N + TOKENS - 1) / TOKENS;
     const int heads = p.Hq + p.Hkv + (dy[2].p ? p.Hkv : 0);
-    p.heads_per_cta = (heads + head_groups(blocks, heads) - 1) / head_groups(blocks, heads);
-    const int groups = (heads + p.heads_per_cta - 1) / p.heads_per_cta;
-    const int grid = static_cast<int>(std::min<long long>(blocks * groups, kBwdCtas));
+    const long long units = blocks * heads;
+    const long long per_cta = std::max(kMinHeads, (units + kBwdCtas - 1) / kBwdCtas);
+    const int grid = static_cast<int>((units + per_cta - 1) / per_cta);
     fa::fa_prep_bwd_kernel<D, IL><<<grid, fa::kRopeThreads, 0, s>>>(
-        dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2], p, static_cast<int>(blocks), groups,
-        part);
+        dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2], p, per_cta, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.wq) return e;
     cudaLaunchConfig_t cfg = {};

@@ -70,14 +70,6 @@ struct PrepOut {
 
 constexpr int kRopeThreads = 256;
 
-__device__ __forceinline__ uint4 ld_row16(const __nv_bfloat16* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -202,14 +194,60 @@ __device__ __forceinline__ int sequence_of(const int* seq_start, int S, int t) {
     return lo;
 }
 
+// Each thread's rows on their way in: SLOTS slots of two 16-byte pieces that
+// it alone writes (with asynchronous copies) and reads, so no barrier is
+// needed and the bytes in flight do not cost registers.
+template <int SLOTS>
+struct RowRing {
+    uint32_t base;  // of this thread's piece 0 in slot 0
+    static constexpr uint32_t PIECE = kRopeThreads * 16u, SLOT = 2u * PIECE;
+    static constexpr int BYTES = SLOTS * static_cast<int>(SLOT);
+
+    __device__ __forceinline__ void put(int slot, int piece, const __nv_bfloat16* src) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + slot * SLOT +
+                                                                       piece * PIECE),
+                     "l"(src)
+                     : "memory");
+    }
+    static __device__ __forceinline__ void commit() {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // All groups but the newest SLOTS - 2 have landed: with SLOTS - 1 of them
+    // committed ahead of the step that reads, that step's.
+    static __device__ __forceinline__ void wait() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 2) : "memory");
+    }
+    __device__ __forceinline__ uint4 get(int slot, int piece) const {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(base + slot * SLOT + piece * PIECE)
+                     : "memory");
+        return v;
+    }
+    static __device__ __forceinline__ int next(int slot) { return slot + 1 == SLOTS ? 0 : slot + 1; }
+};
+
+// The heads [a, z) of part 0, 1, 2 (queries, keys, values) among [h0, h1).
+struct PartRange {
+    int first, count, a, z;
+    __device__ __forceinline__ PartRange(const RopeParams& p, int part, int h0, int h1)
+        : first(part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv),
+          count(part == 0 ? p.Hq : p.Hkv),
+          a(max(h0, first)),
+          z(min(h1, first + count)) {}
+};
+
 // Grid: x over blocks of 256 / (D / 8) tokens, y over groups of heads.  The
 // heads are the Hq query heads, then Hkv key heads, then (with v) Hkv value
 // heads, which are moved unchanged.
 template <int D, bool INTERLEAVED, bool PAGED>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 3)
     fa_prep_kernel(const HeadRows q, const HeadRows k, const HeadRows v, const RopeParams p,
                    const PrepOut out, const PagedDest dst) {
-    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, U = 4;
+    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, SLOTS = 4;
+    __shared__ __align__(16) uint8_t ring_mem[RowRing<SLOTS>::BYTES];
+    const RowRing<SLOTS> ring{smem_u32(ring_mem) + threadIdx.x * 16u};
     const int lane = threadIdx.x & 31;
     const int col = threadIdx.x & (LANES - 1), e0 = 8 * col;
     const long long total = static_cast<long long>(p.B) * p.N;
@@ -218,6 +256,34 @@ __global__ void __launch_bounds__(kRopeThreads)
     if (!active) row = total - 1;
     const long long b = PAGED ? 0 : row / p.N;
     const long long n = PAGED ? row : row - b * p.N;
+    const int heads = p.Hq + p.Hkv + (v.p ? p.Hkv : 0);
+    const int h0 = blockIdx.y * p.heads_per_cta;
+    const int h1 = min(h0 + p.heads_per_cta, heads);
+
+    // The loader runs SLOTS - 1 steps ahead; a step is two heads of one part.
+    int load_part = -1, load_left = 0, load_slot = 0;
+    const __nv_bfloat16* load_src = nullptr;
+    long long load_step = 0;
+    auto load = [&]() {
+        while (load_left == 0 && load_part < 2) {
+            const PartRange r(p, ++load_part, h0, h1);
+            if (r.a >= r.z) continue;
+            const HeadRows& in = load_part == 0 ? q : load_part == 1 ? k : v;
+            load_left = r.z - r.a;
+            load_src = in.p + b * in.sb + n * in.sn + (r.a - r.first) * in.sh + e0;
+            load_step = in.sh;
+        }
+        if (load_left > 0) {
+            ring.put(load_slot, 0, load_src);
+            if (load_left > 1) ring.put(load_slot, 1, load_src + load_step);
+            load_src += 2 * load_step;
+            load_left = max(0, load_left - 2);
+            load_slot = ring.next(load_slot);
+        }
+        ring.commit();
+    };
+#pragma unroll
+    for (int i = 0; i < SLOTS - 1; ++i) load();
 
     long long pos;
     long long page_row = -1;  // row of the token in its page, over all pages; -1: nowhere
@@ -241,57 +307,49 @@ __global__ void __launch_bounds__(kRopeThreads)
     } else {
         pos = p.positions ? p.positions[row] : n;
     }
-    Turn<D, INTERLEAVED> turn;
-    turn.load(p, checked_position(p, pos, active), lane);
-
-    const int heads = p.Hq + p.Hkv + (v.p ? p.Hkv : 0);
-    const int h0 = blockIdx.y * p.heads_per_cta;
-    const int h1 = min(h0 + p.heads_per_cta, heads);
+    pos = checked_position(p, pos, active);
     const bool norm = p.wq != nullptr;
 
+    int slot = 0;
 #pragma unroll 1
-    for (int part = 0; part < 3; ++part) {  // queries, keys, values
-        const int first = part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv;
-        const int count = part == 0 ? p.Hq : p.Hkv;
-        const int a = max(h0, first), z = min(h1, first + count);
-        if (a >= z) continue;
-        const HeadRows& in = part == 0 ? q : part == 1 ? k : v;
-        const __nv_bfloat16* src = in.p + b * in.sb + n * in.sn + (a - first) * in.sh + e0;
-        // Destination of head `a` and the step to the next head.
+    for (int part = 0; part < 3; ++part) {
+        const PartRange r(p, part, h0, h1);
+        if (r.a >= r.z) continue;
+        // Destination of the first head and the step to the next.
         __nv_bfloat16* to;
         long long step;
         bool write = active;
         if constexpr (PAGED) {
             if (part == 0) {
-                to = dst.q_out + (row * p.Hq + a) * D + e0;
+                to = dst.q_out + (row * p.Hq + r.a) * D + e0;
                 step = D;
             } else {
                 write = page_row >= 0;
                 step = static_cast<long long>(D) << dst.page_shift;
                 to = (part == 1 ? dst.k_pages : dst.v_pages) +
-                     (page * p.Hkv + (a - first)) * step + (write ? page_row : 0) * D + e0;
+                     (page * p.Hkv + (r.a - r.first)) * step + (write ? page_row : 0) * D + e0;
             }
         } else {
             step = static_cast<long long>(p.N) * D;
             to = (part == 0 ? out.q : part == 1 ? out.k : out.v) +
-                 (b * count + (a - first)) * step + n * D + e0;
+                 (b * r.count + (r.a - r.first)) * step + n * D + e0;
         }
         if (part == 2) {
 #pragma unroll 1
-            for (int h = a; h < z; h += U) {
-                uint4 w[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (h + u < z) w[u] = ld_row16(src + u * in.sh);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (h + u < z && write) *reinterpret_cast<uint4*>(to + u * step) = w[u];
-                src += U * in.sh;
-                to += U * step;
+            for (int h = r.a; h < r.z; h += 2) {
+                ring.wait();
+                const uint4 w0 = ring.get(slot, 0), w1 = ring.get(slot, 1);
+                slot = ring.next(slot);
+                load();
+                if (write) *reinterpret_cast<uint4*>(to) = w0;
+                if (write && h + 1 < r.z) *reinterpret_cast<uint4*>(to + step) = w1;
+                to += 2 * step;
             }
             continue;
         }
         // y_j = rstd * (x_j * own_j + partner_j * cross_j)
+        Turn<D, INTERLEAVED> turn;
+        turn.load(p, pos, lane);
         float own[8], cross[8];
         const void* wt = part == 0 ? p.wq : p.wk;
 #pragma unroll
@@ -306,15 +364,15 @@ __global__ void __launch_bounds__(kRopeThreads)
             }
         }
 #pragma unroll 1
-        for (int h = a; h < z; h += U) {
-            uint4 w[U];
+        for (int h = r.a; h < r.z; h += 2) {
+            ring.wait();
+            uint4 w[2];
+            w[0] = ring.get(slot, 0);
+            w[1] = h + 1 < r.z ? ring.get(slot, 1) : make_uint4(0u, 0u, 0u, 0u);
+            slot = ring.next(slot);
+            load();
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                w[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (h + u < z) w[u] = ld_row16(src + u * in.sh);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < 2; ++u) {
                 float x[8], xp[8], y[8];
                 widen8(w[u], x);
                 turn.partners(w[u], x, xp);
@@ -328,129 +386,174 @@ __global__ void __launch_bounds__(kRopeThreads)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     y[j] = rstd * (turn.on ? fmaf(x[j], own[j], xp[j] * cross[j]) : x[j] * own[j]);
-                if (h + u < z && write) *reinterpret_cast<uint4*>(to + u * step) = narrow8(y);
+                if (h + u < r.z && write) *reinterpret_cast<uint4*>(to + u * step) = narrow8(y);
             }
-            src += U * in.sh;
-            to += U * step;
+            to += 2 * step;
         }
     }
 }
 
-// Gradients of fa_prep_kernel's training form.  A CTA walks (token block, head
-// group) items; with a norm it leaves its sums of dw for queries and keys in
-// `part` [CTAs][2][D], which fa_dw_reduce_kernel adds up in a fixed order.
+// Gradients of fa_prep_kernel's training form.  The heads of all token blocks
+// are numbered block by block, and CTA c takes numbers [c, c + 1) * per_cta: a
+// few whole blocks and two parts of one.  With a norm it leaves its sums of dw
+// for queries and keys in `part` [CTAs][2][D], which fa_dw_reduce_kernel adds
+// up in a fixed order.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 2)
     fa_prep_bwd_kernel(const HeadRows dyq, const HeadRows dyk, const HeadRows dyv,
                        const HeadRows xq, const HeadRows xk, const HeadRowsOut dq,
                        const HeadRowsOut dk, const HeadRowsOut dv, const RopeParams p,
-                       int token_blocks, int head_groups, float* part_dw) {
-    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, U = 2;
+                       long long per_cta, float* part_dw) {
+    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, SLOTS = 5;
+    __shared__ __align__(16) uint8_t ring_mem[RowRing<SLOTS>::BYTES];
+    const RowRing<SLOTS> ring{smem_u32(ring_mem) + threadIdx.x * 16u};
     const int lane = threadIdx.x & 31;
     const int col = threadIdx.x & (LANES - 1), e0 = 8 * col;
     const long long total = static_cast<long long>(p.B) * p.N;
     const int heads = p.Hq + p.Hkv + (dyv.p ? p.Hkv : 0);
     const bool norm = p.wq != nullptr;
+    const long long first_head = blockIdx.x * per_cta;
+    const long long last_head =
+        min(first_head + per_cta, (total + TOKENS - 1) / TOKENS * heads);
     float dw[2][8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
 
-    const long long items = static_cast<long long>(token_blocks) * head_groups;
+    // An item: the token (b, n) and its heads [h0, h1).
+    struct Item {
+        long long row, b, n;
+        bool active;
+        int h0, h1;
+    };
+    auto item_at = [&](long long at) {
+        Item x;
+        const long long tb = at / heads;
+        x.h0 = static_cast<int>(at - tb * heads);
+        x.h1 = static_cast<int>(min(static_cast<long long>(heads), x.h0 + (last_head - at)));
+        x.row = tb * TOKENS + threadIdx.x / LANES;
+        x.active = x.row < total;
+        if (!x.active) x.row = total - 1;
+        x.b = x.row / p.N;
+        x.n = x.row - x.b * p.N;
+        return x;
+    };
+    // The loader runs SLOTS - 1 steps ahead, over the borders of items.  A
+    // step is a head's gradient and (with a norm) row, or two value heads.
+    long long load_at = first_head;
+    int load_part = -1, load_left = 0, load_slot = 0;
+    const __nv_bfloat16 *load_g = nullptr, *load_x = nullptr;
+    long long load_gs = 0, load_xs = 0;
+    auto load = [&]() {
+        while (load_left == 0 && load_at < last_head) {
+            const Item x = item_at(load_at);
+            if (++load_part == 3) {
+                load_part = -1;
+                load_at += x.h1 - x.h0;
+                continue;
+            }
+            const PartRange r(p, load_part, x.h0, x.h1);
+            if (r.a >= r.z) continue;
+            const HeadRows& dy = load_part == 0 ? dyq : load_part == 1 ? dyk : dyv;
+            const HeadRows& in = load_part == 0 ? xq : xk;
+            load_left = r.z - r.a;
+            load_g = dy.p + x.b * dy.sb + x.n * dy.sn + (r.a - r.first) * dy.sh + e0;
+            load_gs = dy.sh;
+            if (norm) {
+                load_x = in.p + x.b * in.sb + x.n * in.sn + (r.a - r.first) * in.sh + e0;
+                load_xs = in.sh;
+            }
+        }
+        if (load_left > 0) {
+            ring.put(load_slot, 0, load_g);
+            if (load_part == 2) {
+                if (load_left > 1) ring.put(load_slot, 1, load_g + load_gs);
+                load_g += 2 * load_gs;
+                load_left = max(0, load_left - 2);
+            } else {
+                if (norm) ring.put(load_slot, 1, load_x);
+                load_g += load_gs;
+                load_x += load_xs;
+                --load_left;
+            }
+            load_slot = ring.next(load_slot);
+        }
+        ring.commit();
+    };
+#pragma unroll
+    for (int i = 0; i < SLOTS - 1; ++i) load();
+
+    int slot = 0;
 #pragma unroll 1
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const long long tb = it / head_groups;
-        const int h0 = static_cast<int>(it - tb * head_groups) * p.heads_per_cta;
-        const int h1 = min(h0 + p.heads_per_cta, heads);
-        long long row = tb * TOKENS + threadIdx.x / LANES;
-        const bool active = row < total;
-        if (!active) row = total - 1;
-        const long long b = row / p.N, n = row - b * p.N;
+    for (long long at = first_head; at < last_head;) {
+        const Item x = item_at(at);
+        at += x.h1 - x.h0;
         Turn<D, INTERLEAVED> turn;
-        turn.load(p, checked_position(p, p.positions ? p.positions[row] : n, active), lane);
+        turn.load(p, checked_position(p, p.positions ? p.positions[x.row] : x.n, x.active), lane);
 
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
-            const int first = part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv;
-            const int count = part == 0 ? p.Hq : p.Hkv;
-            const int a = max(h0, first), z = min(h1, first + count);
-            if (a >= z) continue;
-            const HeadRows& dy = part == 0 ? dyq : part == 1 ? dyk : dyv;
+            const PartRange r(p, part, x.h0, x.h1);
+            if (r.a >= r.z) continue;
             const HeadRowsOut& dx = part == 0 ? dq : part == 1 ? dk : dv;
-            const __nv_bfloat16* gsrc = dy.p + b * dy.sb + n * dy.sn + (a - first) * dy.sh + e0;
-            __nv_bfloat16* to = dx.p + b * dx.sb + n * dx.sn + (a - first) * dx.sh + e0;
+            __nv_bfloat16* to = dx.p + x.b * dx.sb + x.n * dx.sn + (r.a - r.first) * dx.sh + e0;
             if (part == 2) {
 #pragma unroll 1
-                for (int h = a; h < z; h += 4) {
-                    uint4 w[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (h + u < z) w[u] = ld_row16(gsrc + u * dy.sh);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (h + u < z && active) *reinterpret_cast<uint4*>(to + u * dx.sh) = w[u];
-                    gsrc += 4 * dy.sh;
-                    to += 4 * dx.sh;
+                for (int h = r.a; h < r.z; h += 2) {
+                    ring.wait();
+                    const uint4 w0 = ring.get(slot, 0), w1 = ring.get(slot, 1);
+                    slot = ring.next(slot);
+                    load();
+                    if (x.active) *reinterpret_cast<uint4*>(to) = w0;
+                    if (x.active && h + 1 < r.z) *reinterpret_cast<uint4*>(to + dx.sh) = w1;
+                    to += 2 * dx.sh;
                 }
                 continue;
             }
-            const HeadRows& xr = part == 0 ? xq : xk;
-            const __nv_bfloat16* xsrc =
-                norm ? xr.p + b * xr.sb + n * xr.sn + (a - first) * xr.sh + e0 : nullptr;
             float w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 w[j] = norm ? weight_at(part == 0 ? p.wq : p.wk, p.w_f32, e0 + j) : 1.f;
 #pragma unroll 1
-            for (int h = a; h < z; h += U) {
-                uint4 gr[U], xw[U];
+            for (int h = r.a; h < r.z; ++h) {
+                ring.wait();
+                const uint4 gr = ring.get(slot, 0);
+                uint4 xr = make_uint4(0u, 0u, 0u, 0u);
+                if (norm) xr = ring.get(slot, 1);
+                slot = ring.next(slot);
+                load();
+                float g[8], gp[8], y[8];
+                widen8(gr, g);
+                turn.partners(gr, g, gp);
+                if (turn.on) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    gr[u] = xw[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (h + u < z) {
-                        gr[u] = ld_row16(gsrc + u * dy.sh);
-                        if (norm) xw[u] = ld_row16(xsrc + u * xr.sh);
+                    for (int j = 0; j < 8; ++j)  // the turn's transpose
+                        y[j] = fmaf(g[j], turn.c[j], -turn.sign_of(j) * gp[j] * turn.s[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = g[j];
+                }
+                if (norm) {
+                    float v[8];
+                    widen8(xr, v);
+                    float ss = 0.f, gx = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        ss += v[j] * v[j];
+                        gx += y[j] * w[j] * v[j];
+                    }
+                    ss = row_sum<LANES>(ss);
+                    gx = row_sum<LANES>(gx);
+                    const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
+                    const float along = gx * rstd * (1.f / D);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float xh = v[j] * rstd;
+                        if (x.active) dw[part == 0 ? 0 : 1][j] += y[j] * xh;
+                        y[j] = rstd * (y[j] * w[j] - xh * along);
                     }
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float g[8], gp[8], y[8];
-                    widen8(gr[u], g);
-                    turn.partners(gr[u], g, gp);
-                    if (turn.on) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)  // the turn's transpose
-                            y[j] = fmaf(g[j], turn.c[j], -turn.sign_of(j) * gp[j] * turn.s[j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) y[j] = g[j];
-                    }
-                    if (norm) {
-                        float x[8];
-                        widen8(xw[u], x);
-                        float ss = 0.f, gx = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            ss += x[j] * x[j];
-                            gx += y[j] * w[j] * x[j];
-                        }
-                        ss = row_sum<LANES>(ss);
-                        gx = row_sum<LANES>(gx);
-                        const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
-                        const float along = gx * rstd * (1.f / D);
-                        const bool mine = h + u < z && active;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float xh = x[j] * rstd;
-                            if (mine) dw[part == 0 ? 0 : 1][j] += y[j] * xh;
-                            y[j] = rstd * (y[j] * w[j] - xh * along);
-                        }
-                    }
-                    if (h + u < z && active)
-                        *reinterpret_cast<uint4*>(to + u * dx.sh) = narrow8(y);
-                }
-                gsrc += U * dy.sh;
-                xsrc += U * xr.sh;
-                to += U * dx.sh;
+                if (x.active) *reinterpret_cast<uint4*>(to) = narrow8(y);
+                to += dx.sh;
             }
         }
     }

@@ -8,6 +8,7 @@ fallback path, and a missing library raises ``FaError`` on first use.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -316,6 +317,7 @@ def fa_paged_append(q: int, k: int, v: int, strides, q_weight: int, k_weight: in
         stream or None)
 
 
+@functools.lru_cache(maxsize=1024)
 def fa_paged_workspace_size(S: int, T: int, Hq: int, Hkv: int, d: int, page_size: int,
                             max_pages: int, prefix_len: int, max_new: int) -> int:
     return int(library().fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
@@ -324,8 +326,8 @@ def fa_paged_workspace_size(S: int, T: int, Hq: int, Hkv: int, d: int, page_size
 
 def fa_paged_split_plan(S: int, T: int, Hq: int, Hkv: int, d: int, page_size: int,
                         max_pages: int, prefix_len: int, max_new: int, sm_count: int):
-    """(status, prefix splits, keys per prefix split, own splits) of the host
-    split plan; pure host arithmetic, needs no GPU."""
+    """(status, prefix splits, keys per prefix split, CTAs that share the
+    sequences' keys) of the host split plan; pure host arithmetic, needs no GPU."""
     ps, ch, os_ = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
     st = library().fa_paged_split_plan(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len,
                                        max_new, sm_count, ctypes.byref(ps), ctypes.byref(ch),
@@ -553,15 +555,15 @@ def _rows(name, t, shape, device):
 
 def _exact_tensor(name, t, shape, dtype, device):
     """Data pointer of a contiguous tensor of exactly this shape and type."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _require_cuda(name, t):
@@ -591,23 +593,32 @@ def _norm_rope_args(q_weight, k_weight, rope, d, device):
 
 class _Place:
     """Makes a call's device current and, with a stream of the caller's,
-    allocates on it; `.raw` is the stream's handle."""
+    allocates on it; entering gives the stream's handle.  A single token's call
+    is bound by the host, and torch.cuda.device and current_stream take 4 us of
+    it, so the device is only switched where it differs and the current
+    stream's handle is asked for directly (0.1 us)."""
+    __slots__ = ("guards", "raw")
 
     def __init__(self, device, stream):
-        self.device = torch.cuda.device(device)
-        self.stream = torch.cuda.stream(stream) if stream is not None else None
-        self.raw = (stream or torch.cuda.current_stream(device)).cuda_stream
+        self.guards = ()
+        if torch.cuda.current_device() != device.index:
+            self.guards = (torch.cuda.device(device),)
+        if stream is None:
+            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream: expected device {device}, got {stream.device}")
+            self.guards += (torch.cuda.stream(stream),)
+            self.raw = stream.cuda_stream
 
     def __enter__(self):
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
+        for g in self.guards:
+            g.__enter__()
         return self.raw
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
 
 
 def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cuda", stream=None):
@@ -649,11 +660,11 @@ def qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-6, 
         pos = _exact_tensor("positions", positions, (B, N), torch.int32, device)
     with _Place(device, stream) as s:
         if q_out is None:
-            q_out = torch.empty((B, Hq, N, d), dtype=q.dtype, device=device)
+            q_out = q.new_empty((B, Hq, N, d))
         if k_out is None:
-            k_out = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=device)
+            k_out = q.new_empty((B, Hkv, N, d))
         if v is not None and v_out is None:
-            v_out = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=device)
+            v_out = q.new_empty((B, Hkv, N, d))
         _check(fa_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), v.data_ptr() if v is not None else 0, strides, wq, wk,
             w32, eps, table, rows, width, int(interleaved), pos,
@@ -698,21 +709,21 @@ def qk_norm_rope_backward(dq_out, dk_out, dv_out, q, k, q_weight=None, k_weight=
         pos = _exact_tensor("positions", positions, (B, N), torch.int32, device)
     with _Place(device, stream) as s:
         if dq is None:
-            dq = torch.empty(qs, dtype=torch.bfloat16, device=device)
+            dq = dq_out.new_empty(qs)
         if dk is None:
-            dk = torch.empty(ks, dtype=torch.bfloat16, device=device)
+            dk = dq_out.new_empty(ks)
         if dv is None and dv_out is not None:
-            dv = torch.empty(ks, dtype=torch.bfloat16, device=device)
+            dv = dq_out.new_empty(ks)
         grads = _rows("dq", dq, qs, device) + _rows("dk", dk, ks, device)
         if dv is not None:
             grads += _rows("dv", dv, ks, device)
         dwq = dwk = None
         if wq:
-            dwq = torch.empty(d, dtype=torch.float32, device=device)
-            dwk = torch.empty(d, dtype=torch.float32, device=device)
+            dwq = dq_out.new_empty(d, dtype=torch.float32)
+            dwk = dq_out.new_empty(d, dtype=torch.float32)
             if workspace is None:
-                workspace = torch.empty(max(1, fa_qk_norm_rope_bwd_workspace_size(d)),
-                                        dtype=torch.uint8, device=device)
+                workspace = dq_out.new_empty(max(1, fa_qk_norm_rope_bwd_workspace_size(d)),
+                                             dtype=torch.uint8)
         ws, ws_bytes = _workspace(workspace, device)
         _check(fa_qk_norm_rope_bwd(
             gq, gk, gv, q.data_ptr() if wq else 0, k.data_ptr() if wq else 0, strides, wq, wk,
@@ -772,7 +783,7 @@ def paged_append(q, k, v, k_pages, v_pages, block_table, seq_start, cache_len, r
     wq, wk, w32, table, rows, width = _norm_rope_args(q_weight, k_weight, rope, d, device)
     with _Place(device, stream) as s:
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
+            q_out = q.new_empty((T, Hq, d))
         qo = _exact_tensor("q_out", q_out, (T, Hq, d), torch.bfloat16, device)
         if T:
             _check(fa_paged_append(
@@ -820,9 +831,9 @@ def attention_paged(q, k_pages, v_pages, block_table, seq_start, kv_len, scale: 
     most = T if max_new is None else int(max_new)
     with _Place(device, stream) as s:
         if out is None:
-            out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
+            out = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+            lse = q.new_empty((T, Hq), dtype=torch.float32)
         op = _exact_tensor("out", out, (T, Hq, d), torch.bfloat16, device)
         lp = _exact_tensor("lse", lse, (T, Hq), torch.float32, device)
         if T:
@@ -830,7 +841,7 @@ def attention_paged(q, k_pages, v_pages, block_table, seq_start, kv_len, scale: 
                 need = fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
                                                prefix_len, most)
                 if need:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+                    workspace = q.new_empty(need, dtype=torch.uint8)
             ws, ws_bytes = _workspace(workspace, device)
             _check(fa_fwd_paged(qp, kp, vp, bt, ss, kl, pp, prefix_len, op, lp, S, T, Hq, Hkv, d,
                                 page_size, pages, max_pages, most, scale, ws, ws_bytes, s),

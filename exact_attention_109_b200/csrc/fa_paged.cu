@@ -15,16 +15,19 @@ namespace {
 using fa_host::aligned;
 
 constexpr int kMaxDevices = 64;
-// Work units (CTAs) that the splits aim at, at most: they bound the workspace.
+// CTAs at most: they bound the workspace.
 constexpr long long kMaxPrefixCtas = 512;
-constexpr long long kWantOwnCtas = 592;
-constexpr int kMaxOwnSplits = 256;
+constexpr int kMaxLineCtas = 444;
+// Query rows of a key head for which the prefix joins the line of the sequences.
+constexpr int kLinePrefixRows = 16;
 
 struct Plan {
     int tiles;            // query tiles per prefix CTA
     int row_tiles;        // prefix CTAs along the rows
     int prefix_splits, prefix_chunk;
-    int own_row_tiles, own_splits;
+    bool prefix_in_line;
+    int slots;            // partial results of all rows
+    int line_ctas;
 };
 
 int ilog2(int x) {
@@ -44,55 +47,69 @@ fa_status check_sizes(int S, int T, int Hq, int Hkv, int d, int page_size, int m
     if (static_cast<long long>(T) * Hq > (1ll << 24) || prefix_len > (1 << 30) ||
         static_cast<long long>(max_pages) * page_size > (1ll << 30))
         return FA_ERR_INVALID_ARG;
-    // One CTA per sequence, 16-row tile, key head and split; 32-bit grid.
-    const long long tiles = (static_cast<long long>(max_new) * (Hq / Hkv) + 15) / 16;
-    if (T > 0 && static_cast<double>(S) * tiles * Hkv * kMaxOwnSplits > 2147483647.0)
-        return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 
-// Splits of the prefix: the fewest waves of CTAs (one per SM), a CTA's time
-// being its key blocks plus a fixed part of about three blocks' time (set-up,
-// the first loads, writing its partial result).
-void plan_prefix(Plan& pl, int T, int G, int Hkv, int prefix_len, int sm_count) {
-    pl.prefix_splits = 0;
-    pl.prefix_chunk = 0;
-    pl.row_tiles = 1;
-    pl.tiles = 1;
-    if (prefix_len == 0) return;
+// The prefix's tiles of query rows, and the splits that the workspace has room
+// for.
+Plan plan_rows(int T, int G, int Hkv, int prefix_len) {
+    Plan pl{};
     const long long rows = static_cast<long long>(T) * G;
+    pl.prefix_in_line = prefix_len > 0 && rows <= kLinePrefixRows;
     pl.tiles = rows > 128 ? 2 : 1;
     pl.row_tiles = static_cast<int>((rows + 128 * pl.tiles - 1) / (128 * pl.tiles));
     const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
-    const long long blocks = (prefix_len + 127) / 128;
-    const long long most = std::min(blocks, std::max(1ll, kMaxPrefixCtas / units));
-    long long best = 0, best_cost = 0;
-    for (long long n = 1; n <= most; ++n) {
-        const long long per = (blocks + n - 1) / n;
-        if ((blocks + per - 1) / per != n) continue;  // the last split would be empty
-        const long long cost = ((units * n + sm_count - 1) / sm_count) * (per + 3);
-        if (best == 0 || cost < best_cost) {
-            best = n;
-            best_cost = cost;
-        }
-    }
-    pl.prefix_splits = static_cast<int>(best);
-    pl.prefix_chunk = static_cast<int>((blocks + best - 1) / best) * 128;
+    if (prefix_len > 0 && !pl.prefix_in_line)
+        pl.prefix_splits = static_cast<int>(std::min<long long>(
+            (prefix_len + 127) / 128, std::max(1ll, kMaxPrefixCtas / units)));
+    return pl;
 }
 
-Plan make_plan(int S, int T, int Hq, int Hkv, int page_size, int max_pages, int prefix_len,
+// CTAs of the line: as many as are resident, unless the longest line has less
+// work.
+int line_ctas(const Plan& pl, int S, int G, int Hkv, int d, int page_size, int max_pages,
+              int prefix_len, int max_new, int sm_count) {
+    const double cap = (static_cast<long long>(max_pages) * page_size + 63) / 64;
+    const long long tiles = (static_cast<long long>(max_new) * G + 15) / 16;
+    const double blocks = (static_cast<double>(S) * tiles * cap +
+                           (pl.prefix_in_line ? (prefix_len + 63) / 64 : 0)) * Hkv;
+    const long long per_sm =
+        d == 64 ? fa::OwnTraits<64>::MIN_CTAS : fa::OwnTraits<128>::MIN_CTAS;
+    const long long ctas = std::min<long long>(kMaxLineCtas, per_sm * sm_count);
+    return blocks < ctas ? static_cast<int>(blocks) : static_cast<int>(ctas);
+}
+
+Plan make_plan(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages, int prefix_len,
                int max_new, int sm_count) {
-    Plan pl;
-    const int G = Hq / Hkv;
-    plan_prefix(pl, T, G, Hkv, prefix_len, sm_count);
-    pl.own_row_tiles = static_cast<int>((static_cast<long long>(max_new) * G + 15) / 16);
-    const long long units = static_cast<long long>(S) * pl.own_row_tiles * Hkv;
-    const long long cap = static_cast<long long>(max_pages) * page_size;
-    const long long most =
-        std::min<long long>(kMaxOwnSplits, (cap + fa::kOwnMinChunk - 1) / fa::kOwnMinChunk);
-    pl.own_splits = static_cast<int>(
-        std::max(1ll, std::min(most, (kWantOwnCtas + units - 1) / units)));
+    Plan pl = plan_rows(T, Hq / Hkv, Hkv, prefix_len);
+    pl.line_ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
+                             sm_count);
+    if (pl.prefix_splits > 0) {
+        // The splits with the fewest waves of CTAs (one per SM), a CTA's time
+        // being its key blocks plus a fixed part of about three blocks' time
+        // (set-up, the first loads, writing its partial result).
+        const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
+        const long long blocks = (prefix_len + 127) / 128, most = pl.prefix_splits;
+        long long best_per = 0, best_cost = 0;
+        for (long long n = 0, waves = 1; n < most; ++waves) {
+            n = std::min(most, std::max(1ll, waves * sm_count / units));
+            const long long per = (blocks + n - 1) / n, used = (blocks + per - 1) / per;
+            const long long cost = (units * used + sm_count - 1) / sm_count * (per + 3);
+            if (best_per == 0 || cost < best_cost) {
+                best_per = per;
+                best_cost = cost;
+            }
+        }
+        pl.prefix_splits = static_cast<int>((blocks + best_per - 1) / best_per);
+        pl.prefix_chunk = static_cast<int>(best_per) * 128;
+    }
+    pl.slots = prefix_len == 0 ? 0 : 1 + (pl.prefix_in_line ? 1 : pl.prefix_splits);
     return pl;
+}
+
+// Bytes of the table of pieces in front of the partial results.
+size_t table_bytes(int T, int Hq) {
+    return (static_cast<size_t>(T) * Hq * 2 * sizeof(int2) + 255) / 256 * 256;
 }
 
 // Opts the kernel into its shared memory and checks that the registers it is
@@ -159,11 +176,9 @@ cudaError_t launch_all(const Plan& pl, const CUtensorMap& mk, const CUtensorMap&
                          fa::PrefixTraits<D, 1>::SMEM_BYTES, false, s, mk, mv, mp, prm);
         if (e != cudaSuccess) return e;
     }
-    const long long grid =
-        static_cast<long long>(prm.S) * pl.own_row_tiles * prm.Hkv * pl.own_splits;
-    e = launch(fa::fa_own_kernel<D>, grid, fa::OwnTraits<D>::THREADS,
+    e = launch(fa::fa_own_kernel<D>, pl.line_ctas, fa::OwnTraits<D>::THREADS,
                fa::OwnTraits<D>::SMEM_BYTES, prefix, s, mk, mv, prm);
-    if (e != cudaSuccess || pl.prefix_splits + pl.own_splits == 1) return e;
+    if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(prm.T) * prm.Hq;
     return launch(fa::fa_paged_merge_kernel<D>, (rows + 3) / 4, 128, 0, true, s, prm);
 }
@@ -178,29 +193,26 @@ size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d, int page_si
         T == 0)
         return 0;
     // Enough for any SM count: the splits are bounded by the sizes alone.
-    Plan pl = make_plan(S, T, Hq, Hkv, page_size, max_pages, prefix_len, max_new, 1);
-    long long slots = pl.own_splits;
-    if (prefix_len > 0) {
-        const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
-        slots += std::min<long long>((prefix_len + 127) / 128,
-                                     std::max(1ll, kMaxPrefixCtas / units));
-    }
-    return slots == 1 ? 0 : static_cast<size_t>(slots) * T * Hq * (d + 1) * sizeof(float);
+    const Plan pl = plan_rows(T, Hq / Hkv, Hkv, prefix_len);
+    const int ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
+                               kMaxLineCtas);
+    const size_t slots = prefix_len == 0 ? 0 : 1 + (pl.prefix_in_line ? 1 : pl.prefix_splits);
+    return table_bytes(T, Hq) + (slots * T * Hq + ctas * 2 * 16) * (d + 1) * sizeof(float);
 }
 
 fa_status fa_paged_split_plan(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages,
                               int prefix_len, int max_new, int sm_count, int* prefix_splits,
-                              int* prefix_chunk, int* own_splits) {
-    if (!prefix_splits || !prefix_chunk || !own_splits || sm_count < 1) return FA_ERR_INVALID_ARG;
+                              int* prefix_chunk, int* line_ctas) {
+    if (!prefix_splits || !prefix_chunk || !line_ctas || sm_count < 1) return FA_ERR_INVALID_ARG;
     const fa_status st =
         check_sizes(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len, max_new);
     if (st != FA_OK) return st;
     if (T == 0) return FA_ERR_INVALID_ARG;
     const Plan pl =
-        make_plan(S, T, Hq, Hkv, page_size, max_pages, prefix_len, max_new, sm_count);
+        make_plan(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len, max_new, sm_count);
     *prefix_splits = pl.prefix_splits;
     *prefix_chunk = pl.prefix_chunk;
-    *own_splits = pl.own_splits;
+    *line_ctas = pl.line_ctas;
     return FA_OK;
 }
 
@@ -222,7 +234,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
         return FA_ERR_INVALID_ARG;
     const size_t need = fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
                                                 prefix_len, max_new);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+    if (T > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
         !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_start, 4) ||
         !aligned(kv_len, 4) || !aligned(prefix_pages, 4) || !aligned(workspace, 256))
@@ -233,8 +245,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
     if ((st = fa_host::device(&dev, &err, &sms)) != FA_OK) return st;
     if (!prepare(dev)) return FA_ERR_CUDA;
 
-    const Plan pl = make_plan(S, T, Hq, Hkv, page_size, max_pages, prefix_len, max_new, sms);
-    const int slots = pl.prefix_splits + pl.own_splits;
+    const Plan pl = make_plan(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len, max_new, sms);
+    const size_t rows = static_cast<size_t>(pl.slots) * T * Hq;
     fa::PagedParams prm;
     prm.q = static_cast<const __nv_bfloat16*>(q);
     prm.block_table = block_table;
@@ -243,8 +255,10 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
     prm.prefix_pages = prefix_pages;
     prm.o = static_cast<__nv_bfloat16*>(o);
     prm.lse = lse;
-    prm.part_o = static_cast<float*>(workspace);
-    prm.part_lse = workspace ? prm.part_o + static_cast<size_t>(slots) * T * Hq * d : nullptr;
+    prm.pieces = static_cast<int2*>(workspace);
+    prm.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + table_bytes(T, Hq));
+    prm.part_lse = prm.part_o + (rows + pl.line_ctas * 2 * 16) * d;
+    prm.piece_row = static_cast<long long>(rows);
     prm.err = err;
     prm.S = S;
     prm.T = T;
@@ -261,8 +275,9 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
     prm.prefix_splits = pl.prefix_splits;
     prm.prefix_chunk = pl.prefix_chunk;
     prm.row_tiles = pl.row_tiles;
-    prm.own_splits = pl.own_splits;
-    prm.own_row_tiles = pl.own_row_tiles;
+    prm.prefix_in_line = pl.prefix_in_line;
+    prm.slots = pl.slots;
+    prm.line_ctas = pl.line_ctas;
     prm.scale_log2 = sl2;
 
     const long long planes = static_cast<long long>(num_pages) * Hkv;

@@ -16,7 +16,10 @@
 //  * Own rows (fa_own_kernel).  One sequence's keys serve only its own n * G
 //    rows (a handful), so this part is bound by reading the cache; a 128-row
 //    tile would be mostly padding.  Warps use 16-row mma.sync tiles on keys
-//    streamed through shared memory by TMA, keys split over warps and CTAs.
+//    streamed through shared memory by TMA.  The key blocks of all sequences
+//    and heads form one line that is cut into equal pieces, one per CTA, so
+//    ragged lengths leave no SM idle and the loads never stop between them.
+//    A prefix that 16 rows or fewer read is one more sequence of this line.
 //  * fa_paged_merge_kernel joins the partial results of a row.
 //
 // A page is [page rows][d] per head, contiguous, so one TMA box of
@@ -40,21 +43,32 @@ struct PagedParams {
     const int* prefix_pages;  // [ceil(prefix_len / page)]
     __nv_bfloat16* o;         // [T][Hq][D]
     float* lse;               // [T][Hq], natural log
-    // Partial results of slot x (prefix splits, then own splits):
-    float* part_o;            // [slots][Hkv][R][D], normalised
-    float* part_lse;          // [slots][Hkv][R], base 2; -inf: nothing seen, O not written
+    // Partial results, normalised, with their log-sum-exp (base 2; -inf:
+    // nothing seen, O not written).  Row (x * Hkv + head) * R + i holds query
+    // row i of slot x: the prefix's splits, then (with a prefix) the sequences'
+    // own keys where one CTA had them all.  Behind the slots, row
+    // piece_row + (2 c + w) * 16 + i holds row i of a tile that CTA c of the
+    // line had a part of: its first tile (w = 0) or its last.
+    float* part_o;
+    float* part_lse;
+    long long piece_row;
+    // [2][Hkv][R] (own keys; prefix in the line): how many CTAs had a part of
+    // the row's tile, and (2 c + w) * 16 + i of the first.
+    int2* pieces;
     unsigned int* err;
     int S, T, Hq, Hkv, G, R;  // R = T * G query rows per key head
     int page_shift, box_shift;  // log2 of the page's and of a TMA box's rows
     int num_pages, max_pages, max_new;
     int prefix_len, prefix_splits, prefix_chunk, row_tiles;
-    int own_splits, own_row_tiles;
+    int prefix_in_line;       // the prefix is one more sequence of the line
+    int slots, line_ctas;
     float scale_log2;         // scale * log2(e)
 };
 
-// Keys of one split of a sequence's own rows: at least this many, so that a
-// short sequence is not cut up.
-constexpr int kOwnMinChunk = 256;
+// Key blocks that a CTA of the line takes at least, and what a tile costs
+// beside its keys, in blocks: reading Q, joining the warps, writing.
+constexpr int kLineMinBlocks = 2;
+constexpr int kLineTileBlocks = 2;
 
 // Plane of (page, head) in the page tensors' maps.  A page out of range is
 // reported and mapped behind the tensor, where TMA fills with zeros.
@@ -325,25 +339,24 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
         const int t = warp >> 2, lg = warp & 3;
         const int wrow0 = r0 + 128 * t + lg * 32;  // this warp's first query row
         const int row = wrow0 + lane;
-        // Query rows of the warp into the swizzled tile (rows past R: zeros).
+        // Query rows of the warp into the swizzled tile (rows past R: zeros),
+        // all copies in flight at once: through registers, four at a time, this
+        // took 9 us of cold reads.
         {
             constexpr int LPR = D / 8;  // lanes per row
-            uint8_t* qt = smem + T::Q_OFF + t * T::TILE_BYTES;
+            const uint32_t qt = smem_u32(smem + T::Q_OFF + t * T::TILE_BYTES);
             const int u = lane % LPR;
 #pragma unroll 4
             for (int i = 0; i < LPR; ++i) {
                 const int rr = i * (32 / LPR) + lane / LPR;
-                const int r = wrow0 + rr, local = lg * 32 + rr;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (r < p.R) {
-                    const int tok = r / p.G;
-                    const long long at =
-                        (static_cast<long long>(tok) * p.Hq + head * p.G + (r - tok * p.G)) * D;
-                    w = *reinterpret_cast<const uint4*>(p.q + at + 8 * u);
-                }
-                *reinterpret_cast<uint4*>(qt + (u >> 3) * T::CHUNK_BYTES +
-                                          sw128_offset(local, u & 7)) = w;
+                const int r = min(wrow0 + rr, p.R - 1), local = lg * 32 + rr;
+                const int tok = r / p.G;
+                const long long at =
+                    (static_cast<long long>(tok) * p.Hq + head * p.G + (r - tok * p.G)) * D;
+                cp_async16(qt + (u >> 3) * T::CHUNK_BYTES + sw128_offset(local, u & 7),
+                           p.q + at + 8 * u, wrow0 + rr < p.R ? 16u : 0u);
             }
+            cp_async_wait_all();
             fence_proxy_async_smem();
             mbar_arrive(bar_q);
         }
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
 
 template <int D>
 struct OwnTraits {
-    static constexpr int ROWS = 16;  // query rows per CTA (one mma tile)
+    static constexpr int ROWS = 16;  // query rows per tile (one mma tile)
     static constexpr int BK = 64;    // keys per stage, 16 per warp
     static constexpr int NCW = 4;    // consumer warps
     static constexpr int CHUNKS = D / 64;
@@ -507,12 +520,146 @@ struct OwnTraits {
     static constexpr int THREADS = (NCW + 1) * 32;
     static constexpr int BAR_OFF = NSTAGE * STAGE_BYTES;
     static constexpr int ML_OFF = BAR_OFF + 2 * NSTAGE * 8;      // [NCW][ROWS][3]
-    static constexpr int MISC_OFF = ML_OFF + NCW * ROWS * 3 * 4;
+    static constexpr int SCAN_OFF = ML_OFF + NCW * ROWS * 3 * 4;  // see line_start
+    static constexpr int MISC_OFF = SCAN_OFF + 64;
     static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
     static constexpr int MIN_CTAS = D == 128 ? 2 : 3;
-    static constexpr int RED_STRIDE = D + 8;  // floats; spreads rows over the banks
-    static_assert(NCW * ROWS * RED_STRIDE * 4 <= BAR_OFF, "merge buffer exceeds the stages");
+    static_assert(SCAN_OFF % 8 == 0, "alignment");
+    // The four warps' results meet in the last stage of their tile.
+    static_assert(NCW * ROWS * D * 4 <= STAGE_BYTES, "merge buffer exceeds a stage");
 };
+
+// a / b of numbers that are not negative; a 32-bit division takes a fifth of
+// the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// One sequence of the line, or (s = S) the prefix as seen by all T tokens.
+struct LineSeq {
+    int start, n, len, tiles, blocks;  // first token, tokens, keys, row tiles, key blocks
+    __device__ __forceinline__ int span() const { return blocks + kLineTileBlocks; }  // a tile's
+
+    __device__ __forceinline__ LineSeq() {}
+    __device__ __forceinline__ LineSeq(const PagedParams& p, int s) {
+        if (s == p.S) {
+            start = 0;
+            n = p.prefix_in_line ? p.T : 0;
+            len = p.prefix_len;
+        } else {
+            start = max(0, min(p.seq_start[s], p.T));
+            n = max(start, min(p.seq_start[s + 1], p.T)) - start;
+            const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
+            len = static_cast<int>(
+                max(0ll, min(static_cast<long long>(p.kv_len[s]), cap)));
+        }
+        tiles = static_cast<int>((static_cast<long long>(n) * p.G + 15) / 16);
+        blocks = max(1, (len + 63) / 64);  // a tile without keys still has to be written
+    }
+    __device__ __forceinline__ long long size(const PagedParams& p) const {
+        return static_cast<long long>(tiles) * p.Hkv * span();
+    }
+};
+
+// A tile's share of a CTA: blocks [b0, b1) of row tile rt of (sequence s, head).
+// The line runs over sequences, heads, row tiles (they share keys) and a
+// tile's key blocks and its fixed cost; a CTA that would begin with the latter
+// begins with the next tile.
+struct LineWalk {
+    LineSeq seq;
+    int s, head, rt, b0, b1;
+    long long left;  // blocks that the CTA still has, this share's not counted
+
+    __device__ __forceinline__ LineWalk(const PagedParams& p, int s0, long long rem,
+                                        long long quota)
+        : seq(p, s0), s(s0), left(quota) {
+        const long long tile = quotient(rem, seq.span());
+        b0 = static_cast<int>(rem - tile * seq.span());
+        head = static_cast<int>(quotient(tile, seq.tiles));
+        rt = static_cast<int>(tile - static_cast<long long>(head) * seq.tiles);
+        take();
+    }
+    __device__ __forceinline__ bool empty() const { return b0 >= seq.blocks; }
+    __device__ __forceinline__ bool whole() const { return b0 == 0 && b1 >= seq.blocks; }
+    __device__ __forceinline__ void take() {
+        b1 = static_cast<int>(min(static_cast<long long>(seq.span()), b0 + left));
+        left -= b1 - b0;
+    }
+    // To the next share; false at the end of the CTA's blocks or of the line.
+    __device__ __forceinline__ bool next(const PagedParams& p) {
+        if (left <= 0) return false;
+        b0 = 0;
+        if (++rt == seq.tiles) {
+            rt = 0;
+            if (++head == p.Hkv) {
+                head = 0;
+                do {
+                    if (++s > p.S) return false;
+                    seq = LineSeq(p, s);
+                } while (seq.tiles == 0);
+            }
+        }
+        take();
+        return true;
+    }
+    // Keys [first, second) of this share that the tile's last token sees.
+    __device__ __forceinline__ int2 keys(const PagedParams& p) const {
+        int seen = seq.len;
+        if (s < p.S) {
+            const int last = (min((rt + 1) * 16, seq.n * p.G) - 1) / p.G;
+            seen = max(0, min(seq.len, seq.len - seq.n + last + 1));
+        }
+        const int beg = min(b0 * 64, seen);
+        return make_int2(beg, min(b1 * 64, seen));
+    }
+};
+
+// Where this CTA's share of the line begins: sequence `s`, block `rem` of it.
+// All threads sum the sequences' sizes (contiguous runs of them); false: the
+// CTA has none.  scan: 8 long longs of shared memory.
+template <int THREADS>
+__device__ __forceinline__ bool line_start(const PagedParams& p, long long* scan, int& s,
+                                           long long& rem, long long& quota) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int count = p.S + 1, per = (count + THREADS - 1) / THREADS;
+    const int a = min(count, static_cast<int>(threadIdx.x) * per), z = min(count, a + per);
+    long long sum = 0;
+#pragma unroll 4
+    for (int i = a; i < z; ++i) sum += LineSeq(p, i).size(p);
+    long long upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    long long total = 0, before = upto - sum;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    quota = max(static_cast<long long>(kLineMinBlocks), quotient(total + gridDim.x - 1, gridDim.x));
+    const long long pos = blockIdx.x * quota;
+    __syncthreads();
+    if (pos >= before && pos < before + sum) {
+        long long at = before;
+        for (int i = a; i < z; ++i) {
+            const long long size = LineSeq(p, i).size(p);
+            if (pos >= at && pos < at + size) {
+                scan[0] = i;
+                scan[1] = pos - at;
+            }
+            at += size;
+        }
+    }
+    __syncthreads();
+    s = static_cast<int>(scan[0]);
+    rem = scan[1];
+    return pos < total;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -587,10 +734,10 @@ __device__ __forceinline__ void add_visible(const uint8_t* v, int r, int col,
     }
 }
 
-// One CTA: 16 query rows of one sequence and key head against one split of
-// the sequence's own keys.  Row r of a sequence is head r % G of its new token
-// r / G.  Each of four warps takes 16 keys of every 64-key stage and keeps its
-// own running maximum, sum and O; they are merged at the end.
+// One CTA: an equal share of the line, tile after tile.  Row r of a sequence is
+// head r % G of its new token r / G.  Each of four warps takes 16 keys of every
+// 64-key stage and keeps its own running maximum, sum and O; they are merged
+// at the end of a tile's share.
 template <int D>
 __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     fa_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -602,60 +749,10 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     uint64_t* empty = full + T::NSTAGE;
     float* red_ml = reinterpret_cast<float*>(smem + T::ML_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::MISC_OFF);
+    volatile int* carry_on = abort_flag + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool direct = p.prefix_splits == 0 && p.own_splits == 1;
 
     grid_launch_dependents();
-    int idx = blockIdx.x;
-    const int split = idx % p.own_splits;
-    idx /= p.own_splits;
-    const int head = idx % p.Hkv;
-    idx /= p.Hkv;
-    const int rt = idx % p.own_row_tiles;
-    const int s = idx / p.own_row_tiles;
-    const int start = max(0, min(p.seq_start[s], p.T));
-    const int n = max(start, min(p.seq_start[s + 1], p.T)) - start;
-    const int given = p.kv_len[s];
-    const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
-    const int len = static_cast<int>(max(0ll, min(static_cast<long long>(given), cap)));
-    if (threadIdx.x == 0 && n > 0 && (given != len || n > p.max_new)) atomicOr(p.err, kErrIndex);
-    const int rows = n * p.G, r0 = rt * T::ROWS;
-
-    int kbeg = 0, kend = 0;
-    if (r0 < rows) {
-        const int last = (min(r0 + T::ROWS, rows) - 1) / p.G;  // the tile's last token
-        const int kvis = max(0, min(len, len - n + last + 1));
-        const int per = (len + p.own_splits - 1) / p.own_splits;
-        const int chunk = max(kOwnMinChunk, (per + T::BK - 1) / T::BK * T::BK);
-        kbeg = min(static_cast<long long>(split) * chunk, static_cast<long long>(kvis));
-        kend = static_cast<int>(min(static_cast<long long>(kbeg) + chunk,
-                                    static_cast<long long>(kvis)));
-    }
-    const int nblk = (kend - kbeg + T::BK - 1) / T::BK;
-    // Row r of the tile: its output row, and its row among the partials.
-    auto out_row = [&](int r) {
-        const int i = (r0 + r) / p.G;
-        return static_cast<long long>(start + i) * p.Hq + head * p.G + (r0 + r - i * p.G);
-    };
-    auto part_row = [&](int r) {
-        return (static_cast<long long>(p.prefix_splits + split) * p.Hkv + head) * p.R +
-               static_cast<long long>(start) * p.G + r0 + r;
-    };
-
-    if (nblk == 0) {
-        // No key in this split: an empty partial, or the empty row's result.
-        for (int i = threadIdx.x; i < T::ROWS * (D / 8); i += T::THREADS) {
-            const int r = i / (D / 8), u = i % (D / 8);
-            if (r0 + r >= rows) continue;
-            if (direct)
-                *reinterpret_cast<uint4*>(p.o + out_row(r) * D + 8 * u) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            if (u == 0) (direct ? p.lse[out_row(r)] : p.part_lse[part_row(r)]) = -INFINITY;
-        }
-        grid_dependency_wait();
-        return;
-    }
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < T::NSTAGE; ++i) {
             mbar_init(&full[i], 1);
@@ -663,39 +760,66 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
         }
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
     }
-    __syncthreads();
+    // Lengths and counts out of range are reported once.
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.S; i += T::THREADS) {
+            const LineSeq q(p, i);
+            if (q.n > 0 && (p.kv_len[i] != q.len || q.n > p.max_new)) atomicOr(p.err, kErrIndex);
+        }
+    int s0;
+    long long rem, quota;
+    const bool any = line_start<T::THREADS>(p, reinterpret_cast<long long*>(smem + T::SCAN_OFF),
+                                            s0, rem, quota);
+    if (!any) {
+        grid_dependency_wait();
+        return;
+    }
     const AbortState st{abort_flag, p.err};
+    LineWalk walk(p, s0, rem, quota);
+    if (walk.empty() && !walk.next(p)) {
+        grid_dependency_wait();
+        return;
+    }
 
     if (warp == T::NCW) {
         // ------------------------------------------------ producer
         const int box = 1 << p.box_shift, nb = T::BK >> p.box_shift;
         const int b = lane / (2 * T::CHUNKS), c = (lane >> 1) % T::CHUNKS, h = lane & 1;
-        auto key_of = [&](int j) { return kbeg + j * T::BK + (b << p.box_shift); };
-        auto wants = [&](int j) { return b < nb && j < nblk && key_of(j) < kend; };
-        const int* table = p.block_table + static_cast<long long>(s) * p.max_pages;
-        int page = wants(0) ? table[key_of(0) >> p.page_shift] : 0;
         int issued = 0;
-        for (int j = 0; j < nblk; ++j) {
-            const int slot = j % T::NSTAGE;
-            const bool mine = wants(j);
-            const int z = mine ? page_plane(p, page, head) : 0;
-            const int y = key_of(j) & ((1 << p.page_shift) - 1);
-            const int boxes = min(nb, (kend - kbeg - j * T::BK + box - 1) >> p.box_shift);
-            if (wants(j + 1)) page = table[key_of(j + 1) >> p.page_shift];
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(&empty[slot], ((j / T::NSTAGE) & 1) ^ 1u, st)))
-                break;
-            if (lane == 0)
-                mbar_arrive_expect_tx(&full[slot],
-                                      static_cast<uint32_t>(boxes) * box * T::CHUNKS * 256u);
-            __syncwarp();
-            if (mine)
-                tma_load_3d(smem + slot * T::STAGE_BYTES + h * T::TILE_BYTES +
-                                c * T::CHUNK_BYTES + (b << p.box_shift) * 128,
-                            h ? &tmV : &tmK, &full[slot], c * 64, y, z);
-            issued = j + 1;
-        }
+        bool ok = true;
+        do {
+            const int2 keys = walk.keys(p);
+            const int nblk = (keys.y - keys.x + T::BK - 1) / T::BK;
+            auto key_of = [&](int j) { return keys.x + j * T::BK + (b << p.box_shift); };
+            auto wants = [&](int j) { return b < nb && j < nblk && key_of(j) < keys.y; };
+            const int* table = walk.s == p.S ? p.prefix_pages
+                                             : p.block_table +
+                                                   static_cast<long long>(walk.s) * p.max_pages;
+            int page = wants(0) ? table[key_of(0) >> p.page_shift] : 0;
+            for (int j = 0; j < nblk && ok; ++j) {
+                const int slot = issued % T::NSTAGE;
+                const bool mine = wants(j);
+                const int z = mine ? page_plane(p, page, walk.head) : 0;
+                const int y = key_of(j) & ((1 << p.page_shift) - 1);
+                const int boxes = min(nb, (keys.y - keys.x - j * T::BK + box - 1) >> p.box_shift);
+                if (wants(j + 1)) page = table[key_of(j + 1) >> p.page_shift];
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&empty[slot], ((issued / T::NSTAGE) & 1) ^ 1u, st));
+                if (!ok) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[slot],
+                                          static_cast<uint32_t>(boxes) * box * T::CHUNKS * 256u);
+                __syncwarp();
+                if (mine)
+                    tma_load_3d(smem + slot * T::STAGE_BYTES + h * T::TILE_BYTES +
+                                    c * T::CHUNK_BYTES + (b << p.box_shift) * 128,
+                                h ? &tmV : &tmK, &full[slot], c * 64, y, z);
+                ++issued;
+            }
+        } while (ok && walk.next(p));
         // Do not leave with copies in flight.
         for (int j = max(0, issued - T::NSTAGE); j < issued; ++j)
             mbar_wait_bounded(&full[j % T::NSTAGE], (j / T::NSTAGE) & 1);
@@ -705,13 +829,60 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
 
     // ---------------------------------------------------- consumers
     const int rq = lane >> 2, cq = lane & 3;  // fragment row and column group
+    // This warp's 16 keys of a stage: ldmatrix row of each lane.
+    const int key_k = 16 * warp + ((lane >> 4) << 3) + (lane & 7);  // K: keys by matrix pair
+    const int unit_k = (lane >> 3) & 1;
+    const int key_v = 16 * warp + (((lane >> 3) & 1) << 3) + (lane & 7);
+    const int unit_v = lane >> 4;
+    int done = 0;  // stages read so far
+    bool ok = true, first = true;
+    do {
+    const LineSeq& seq = walk.seq;
+    const int start = seq.start, n = seq.n, len = seq.len, head = walk.head;
+    const int rows = n * p.G, r0 = walk.rt * T::ROWS;
+    const bool prefix = walk.s == p.S;
+    const int2 keys = walk.keys(p);
+    const int kbeg = keys.x, kend = keys.y, nblk = (kend - kbeg + T::BK - 1) / T::BK;
+    // Row r of the tile: its output row, and its row among the partials.
+    auto out_row = [&](int r) {
+        const int i = (r0 + r) / p.G;
+        return static_cast<long long>(start + i) * p.Hq + head * p.G + (r0 + r - i * p.G);
+    };
+    const bool whole = walk.whole();
+    const bool direct = whole && p.prefix_len == 0;
+    const long long part0 =
+        whole ? (static_cast<long long>(prefix ? 0 : p.slots - 1) * p.Hkv + head) * p.R +
+                    static_cast<long long>(start) * p.G + r0
+              : p.piece_row + (2ll * blockIdx.x + (first ? 0 : 1)) * T::ROWS;
+    if (walk.b0 == 0 && threadIdx.x < T::ROWS && r0 + static_cast<int>(threadIdx.x) < rows) {
+        // The tile's later blocks are the next CTAs', `quota` for each.
+        const int rest = seq.blocks - walk.b1;
+        const int2 d = make_int2(
+            rest <= 0 ? 1 : 2 + static_cast<int>(quotient(rest - 1, quota)),
+            (2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1)) * T::ROWS + threadIdx.x);
+        p.pieces[(static_cast<long long>(prefix) * p.Hkv + head) * p.R +
+                 static_cast<long long>(start) * p.G + r0 + threadIdx.x] = d;
+    }
+    first = false;
+    if (nblk == 0) {
+        // No key in this share: an empty partial, or the empty row's result.
+        for (int i = threadIdx.x; i < T::ROWS * (D / 8); i += T::NCW * 32) {
+            const int r = i / (D / 8), u = i % (D / 8);
+            if (r0 + r >= rows) break;  // i rises with r
+            if (direct)
+                *reinterpret_cast<uint4*>(p.o + out_row(r) * D + 8 * u) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            if (u == 0) (direct ? p.lse[out_row(r)] : p.part_lse[part0 + r]) = -INFINITY;
+        }
+        continue;
+    }
     uint32_t qa[D / 16][4];
     int lim[2];  // last visible key of rows rq and rq + 8
-    const int lim0 = len - n + r0 / p.G;  // and of the tile's first row
+    const int lim0 = prefix ? len : len - n + r0 / p.G;  // and of the tile's first row
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int r = r0 + rq + 8 * x;
-        lim[x] = r < rows ? min(len, len - n + r / p.G + 1) - 1 : -1;
+        lim[x] = r >= rows ? -1 : prefix ? len - 1 : min(len, len - n + r / p.G + 1) - 1;
         const __nv_bfloat16* src = p.q + (r < rows ? out_row(rq + 8 * x) : 0) * D + 2 * cq;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -726,15 +897,10 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
 
-    // This warp's 16 keys of a stage: ldmatrix row of each lane.
-    const int key_k = 16 * warp + ((lane >> 4) << 3) + (lane & 7);  // K: keys by matrix pair
-    const int unit_k = (lane >> 3) & 1;
-    const int key_v = 16 * warp + (((lane >> 3) & 1) << 3) + (lane & 7);
-    const int unit_v = lane >> 4;
-    bool ok = true;
-    for (int j = 0; j < nblk; ++j) {
-        const int slot = j % T::NSTAGE;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (j / T::NSTAGE) & 1, st));
+    int slot = 0;
+    for (int j = 0; j < nblk; ++j, ++done) {
+        slot = done % T::NSTAGE;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (done / T::NSTAGE) & 1, st));
         if (!ok) break;
         const uint32_t kt = smem_u32(smem + slot * T::STAGE_BYTES);
         const int j0 = kbeg + j * T::BK + 16 * warp;  // the warp's first key
@@ -826,11 +992,12 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
+        if (lane == 0 && j + 1 < nblk) mbar_arrive(&empty[slot]);
     }
 
     // Row sums over the four lanes of a row, then the four warps' results
-    // through shared memory (every stage has been read: the barrier below).
+    // through the tile's last stage, which is given back only after that.  Its
+    // 8-float units are swapped by row, so that the writes meet every bank.
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -838,7 +1005,7 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
             l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
             lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], d);
         }
-    float* red = reinterpret_cast<float*>(smem);  // [NCW][ROWS][RED_STRIDE]
+    float* red = reinterpret_cast<float*>(smem + slot * T::STAGE_BYTES);  // [NCW][ROWS][D]
     named_bar_sync(1, T::NCW * 32);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -850,10 +1017,13 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
         }
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(red + r * T::RED_STRIDE + 8 * i + 2 * cq) =
+            *reinterpret_cast<float2*>(red + r * D + 8 * (i ^ (rq & 7)) + 2 * cq) =
                 make_float2(o[i][2 * x], o[i][2 * x + 1]);
     }
+    // One answer for all warps, so that none waits here for one that gave up.
+    if (threadIdx.x == 0) *carry_on = *abort_flag == 0;
     named_bar_sync(1, T::NCW * 32);
+    ok = *carry_on != 0;
     for (int i = threadIdx.x; i < T::ROWS * (D / 4); i += T::NCW * 32) {
         const int r = i / (D / 4), e4 = (i % (D / 4)) * 4;
         if (r0 + r >= rows) break;  // i rises with r
@@ -868,8 +1038,8 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
             // A warp that saw nothing has l = O = 0; one whose scores were all
             // NaN has m = -inf too, and its NaN must reach the row.
             const float f = ml[0] == -INFINITY ? 1.f : ex2_approx(ml[0] - M);
-            const float4 x = *reinterpret_cast<const float4*>(red + (w * T::ROWS + r) *
-                                                                        T::RED_STRIDE + e4);
+            const float4 x = *reinterpret_cast<const float4*>(
+                red + (w * T::ROWS + r) * D + 8 * ((e4 >> 3) ^ (r & 7)) + (e4 & 7));
             L += f * ml[1];
             Lr += f * ml[2];
             a.x += f * x.x;
@@ -887,11 +1057,15 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
             *reinterpret_cast<uint2*>(p.o + out_row(r) * D + e4) = w;
             if (e4 == 0) p.lse[out_row(r)] = lse2 * 0.6931471805599453f;
         } else {
-            *reinterpret_cast<float4*>(p.part_o + part_row(r) * D + e4) =
+            *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + e4) =
                 make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-            if (e4 == 0) p.part_lse[part_row(r)] = lse2;
+            if (e4 == 0) p.part_lse[part0 + r] = lse2;
         }
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    } while (ok && walk.next(p));
     // The merge waits for this grid only, so this grid ends after the prefix
     // grid (which it was allowed to overtake).
     grid_dependency_wait();
@@ -899,61 +1073,133 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
 
 // ------------------------------------------------------------------ merge
 
-// One warp per output row (token, query head): with w_x = 2^(lse_x - M) over
-// the row's slots, O = sum_x w_x O_x / sum_x w_x.  A slot with nothing seen
-// has weight 0 and its O is not read.
-template <int D>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
-    constexpr int PER = D / 32;
-    const int slots = p.prefix_splits + p.own_splits;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
-    grid_dependency_wait();
-    if (row >= static_cast<long long>(p.T) * p.Hq) return;
-    const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row % p.Hq);
-    if (t < p.seq_start[0] || t >= p.seq_start[p.S]) return;  // no sequence's row
-    const int head = hq / p.G;
-    const long long r = static_cast<long long>(head) * p.R + static_cast<long long>(t) * p.G +
-                        (hq - head * p.G);
-    const long long step = static_cast<long long>(p.Hkv) * p.R;
-    float M = -INFINITY;
-    for (int x = lane; x < slots; x += 32) M = fmaxf(M, p.part_lse[r + x * step]);
+// A row's partial results so far: O and L relative to 2^M.
+template <int PER>
+struct RowSum {
+    float M = -INFINITY, L = 0.f, acc[PER];
+    __device__ __forceinline__ RowSum() {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    float L = 0.f, acc[PER];
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    }
+    // Adds up to U partial results: O values in v, and lane x's log-sum-exp of
+    // the x-th in ls.  One with nothing seen (-inf) has weight 0, and its O was
+    // never written.
+    template <int U>
+    __device__ __forceinline__ void add(const float (&v)[U][PER], float ls) {
+        float m = ls;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    const float* po = p.part_o + r * D + lane * PER;
-#pragma unroll 4
-    for (int x = 0; x < slots; ++x) {
-        const float ls = p.part_lse[r + x * step];
-        if (ls == -INFINITY) continue;
-        const float w = ex2_approx(ls - M);
-        L += w;
-        if constexpr (PER == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(po + x * step * D);
-            acc[0] += w * v.x;
-            acc[1] += w * v.y;
-            acc[2] += w * v.z;
-            acc[3] += w * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(po + x * step * D);
-            acc[0] += w * v.x;
-            acc[1] += w * v.y;
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float M1 = fmaxf(M, m);
+        const float f = M == M1 ? 1.f : ex2_approx(M - M1);
+        M = M1;
+        L *= f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] *= f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float l = __shfl_sync(0xffffffffu, ls, u);
+            if (l == -INFINITY) continue;
+            const float w = ex2_approx(l - M);
+            L += w;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] += w * v[u][i];
         }
     }
-    const bool none = L == 0.f;
-    const float inv = none ? 0.f : 1.f / L;
+};
+
+// One warp per output row (token, query head): with w_x = 2^(lse_x - M) over
+// the row's partial results, O = sum_x w_x O_x / sum_x w_x.  What this costs is
+// its chain of dependent reads, so the prefix's first splits, whose places are
+// known, are read at once with the row's table entry, and its first pieces
+// before any of them is added up.
+template <int D>
+__global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParams p) {
+    constexpr int PER = D / 32, U = 8, V = 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
+    const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - 1ll * t * p.Hq);
+    const int head = hq / p.G, g = hq - head * p.G;
+    const bool mine = row < static_cast<long long>(p.T) * p.Hq && t >= p.seq_start[0] &&
+                      t < p.seq_start[p.S];  // else no sequence's row
+    const long long plane_row = static_cast<long long>(head) * p.R +
+                                static_cast<long long>(t) * p.G + g;
+    const long long step = static_cast<long long>(p.Hkv) * p.R;
+    grid_dependency_wait();
+    if (!mine) return;
+    // Where starts are out of order a row may have no tile: its values are
+    // unspecified, but no read leaves the workspace.
+    auto pieces_of = [&](int kind) {
+        int2 d = p.pieces[kind * step + plane_row];
+        d.y = max(0, min(d.y, 32 * p.line_ctas - 1));
+        d.x = max(1, min(d.x, p.line_ctas - (d.y >> 5)));
+        return d;
+    };
+    auto load = [&](float (&v)[PER], long long r) {
+        const float* src = p.part_o + r * D + lane * PER;
+        if constexpr (PER == 4)
+            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+        else
+            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+    };
+    const int2 own = pieces_of(0);
+    int2 pre = make_int2(0, 0);
+    if (p.prefix_in_line) pre = pieces_of(1);
+    auto load_splits = [&](int x0, float (&v)[U][PER]) {
+        const int n = min(U, p.prefix_splits - x0);
+        const long long r = plane_row + x0 * step;
+        float ls = -INFINITY;
+        if (lane < n) ls = p.part_lse[r + lane * step];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < n) load(v[u], r + u * step);
+        return ls;
+    };
+    auto load_pieces = [&](int x0, float (&v)[V][PER]) {
+        const int n = min(V, pre.x + own.x - x0);
+        long long at = 0;
+        float ls = -INFINITY;
+        if (lane < n) {
+            int x = x0 + lane;
+            const bool of_own = x >= pre.x;
+            const int2 d = of_own ? own : pre;
+            if (of_own) x -= pre.x;
+            at = d.x == 1 ? plane_row + (of_own ? p.slots - 1 : 0) * step
+                          : p.piece_row + (x == 0 ? d.y : ((d.y >> 5) + x) * 32 + (d.y & 15));
+            ls = p.part_lse[at];
+        }
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const long long r = __shfl_sync(0xffffffffu, at, u);
+            if (u < n) load(v[u], r);
+        }
+        return ls;
+    };
+    RowSum<PER> sum;
+    float splits[U][PER], pieces[V][PER];
+    float split_ls = load_splits(0, splits);
+    if (p.prefix_len == 0 && own.x == 1) return;  // written by its CTA
+    float piece_ls = load_pieces(0, pieces);
+    for (int x = 0; x < p.prefix_splits;) {
+        sum.add(splits, split_ls);
+        if ((x += U) < p.prefix_splits) split_ls = load_splits(x, splits);
+    }
+    for (int x = 0; x < pre.x + own.x;) {
+        sum.add(pieces, piece_ls);
+        if ((x += V) < pre.x + own.x) piece_ls = load_pieces(x, pieces);
+    }
+    const bool none = sum.L == 0.f;
+    const float inv = none ? 0.f : 1.f / sum.L;
     __nv_bfloat16* orow = p.o + row * D + lane * PER;
     if constexpr (PER == 4) {
         uint2 w;
-        w.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        w.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+        w.x = pack_bf16x2(sum.acc[0] * inv, sum.acc[1] * inv);
+        w.y = pack_bf16x2(sum.acc[2] * inv, sum.acc[3] * inv);
         *reinterpret_cast<uint2*>(orow) = w;
     } else {
-        *reinterpret_cast<uint32_t*>(orow) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        *reinterpret_cast<uint32_t*>(orow) = pack_bf16x2(sum.acc[0] * inv, sum.acc[1] * inv);
     }
-    if (lane == 0) p.lse[row] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    if (lane == 0)
+        p.lse[row] = none ? -INFINITY : (sum.M + log2f(sum.L)) * 0.6931471805599453f;
 }
 
 }  // namespace fa

@@ -204,10 +204,7 @@ struct RowRing {
     static constexpr int BYTES = SLOTS * static_cast<int>(SLOT);
 
     __device__ __forceinline__ void put(int slot, int piece, const __nv_bfloat16* src) const {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + slot * SLOT +
-                                                                       piece * PIECE),
-                     "l"(src)
-                     : "memory");
+        cp_async16(base + slot * SLOT + piece * PIECE, src);
     }
     static __device__ __forceinline__ void commit() {
         asm volatile("cp.async.commit_group;" ::: "memory");

@@ -490,7 +490,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v,
  *   o         [T,Hq,d] bf16 and lse [T,Hq] fp32, written.  A row that sees no
  *             key gets O = 0, LSE = -inf.
  *   workspace >= fa_paged_workspace_size(...) bytes, 256-byte aligned,
- *             clobbered; may be NULL when that is 0.
+ *             clobbered; may be NULL when T = 0.
  * Query head h reads key head h / (Hq / Hkv).  Cached rows that a token does
  * not see may hold anything, infinities and NaN included, and never reach it.
  * Weights are rounded to bf16 for P V and O is normalised by their sum, as in
@@ -511,14 +511,15 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
 
 /*
  * fa_paged_split_plan -- the work split fa_fwd_paged uses on a GPU with
- * `sm_count` SMs: splits of the prefix (0: none) with prefix_chunk keys each
- * (a multiple of 128), and splits of every sequence's own keys.  Host
+ * `sm_count` SMs: splits of the prefix with prefix_chunk keys each (a multiple
+ * of 128), 0 when there is no prefix or so few rows that it is read like one
+ * more sequence; and the CTAs that share the sequences' keys equally.  Host
  * arithmetic only; touches no GPU.
  */
 fa_status fa_paged_split_plan(int S, int T, int Hq, int Hkv, int d,
                               int page_size, int max_pages, int prefix_len,
                               int max_new, int sm_count, int* prefix_splits,
-                              int* prefix_chunk, int* own_splits);
+                              int* prefix_chunk, int* line_ctas);
 
 /*
  * fa_get_device_error -- synchronises `stream`, then reads and clears the

@@ -71,14 +71,15 @@ def test_split_plan_covers_the_keys_within_the_workspace(S, max_new, Hq, Hkv, P,
             size = (S, T, Hq, Hkv, d, page_size, max_pages, P, max_new)
             have = fa.fa_paged_workspace_size(*size)
             for sms in (1, 80, 148, 1000):
-                st, splits, chunk, own = fa.fa_paged_split_plan(*size, sms)
-                assert st == fa.FA_OK and own >= 1
-                assert (splits == 0) == (P == 0)
-                if P:
+                st, splits, chunk, ctas = fa.fa_paged_split_plan(*size, sms)
+                assert st == fa.FA_OK and 1 <= ctas <= 3 * sms
+                in_line = T * Hq // Hkv <= 16
+                assert (splits == 0) == (P == 0 or in_line)
+                if splits:
                     assert chunk % 128 == 0 and (splits - 1) * chunk < P <= splits * chunk
-                assert own == 1 or (own - 1) * 256 < max_pages * page_size
-                slots = splits + own
-                assert slots == 1 or slots * T * Hq * (d + 1) * 4 <= have
+                slots = 0 if P == 0 else 1 + (1 if in_line else splits)
+                rows = slots * T * Hq + ctas * 2 * 16
+                assert 2 * T * Hq * 8 + rows * (d + 1) * 4 <= have
 
 
 def test_split_plan_refuses_what_the_call_refuses():

@@ -8,7 +8,6 @@ fallback path, and a missing library raises ``FaError`` on first use.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -317,7 +316,6 @@ def fa_paged_append(q: int, k: int, v: int, strides, q_weight: int, k_weight: in
         stream or None)
 
 
-@functools.lru_cache(maxsize=1024)
 def fa_paged_workspace_size(S: int, T: int, Hq: int, Hkv: int, d: int, page_size: int,
                             max_pages: int, prefix_len: int, max_new: int) -> int:
     return int(library().fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
@@ -538,87 +536,39 @@ def attention_backward_bias(q, k, v, bias, out, lse, dO, causal: bool, scale: fl
 
 # ------------------------------------------------ before attention, paged cache
 
-def _rows(name, t, shape, device):
-    """Element strides of a bf16 tensor whose last dimension is contiguous
-    (a dimension of one element gets stride 0)."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return [s if n > 1 else 0 for s, n in zip(st[:-1], shape[:-1])]
+_binding = None
 
 
-def _exact_tensor(name, t, shape, dtype, device):
-    """Data pointer of a contiguous tensor of exactly this shape and type."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name}: must be contiguous")
+def _native():
+    """The compiled marshalling of the calls below (raises when it has not been
+    built): a server makes them once per layer and token, so their host time
+    counts."""
+    global _binding
+    if _binding is None:
+        library()
+        try:
+            from . import _fa_binding
+        except ImportError as e:
+            raise FaError(FA_ERR_UNSUPPORTED,
+                          f"_fa_binding not built (run __graft_entry__.build()): {e}") from e
+        _fa_binding.set_status_error(FaError)
+        _binding = _fa_binding
+    return _binding
 
 
-def _require_cuda(name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    return t.device
+def _on(stream, device):
+    """Makes the caller's stream, which has to be on this device, current."""
+    if stream.device != device:
+        raise ValueError(f"stream: expected device {device}, got {stream.device}")
+    return torch.cuda.stream(stream)
 
 
-def _norm_rope_args(q_weight, k_weight, rope, d, device):
-    """(q_weight, k_weight, is fp32, table, its rows, its width) for the C calls."""
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight: give both or neither")
-    wq = wk = w32 = 0
-    if q_weight is not None:
-        if q_weight.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError(f"q_weight: expected bfloat16 or float32, got {q_weight.dtype}")
-        wq = _exact_tensor("q_weight", q_weight, (d,), q_weight.dtype, device)
-        wk = _exact_tensor("k_weight", k_weight, (d,), q_weight.dtype, device)
-        w32 = int(q_weight.dtype == torch.float32)
-    if rope is None:
-        return wq, wk, w32, 0, 0, 0
-    if rope.dim() != 3 or rope.shape[2] != 2:
-        raise ValueError("rope: expected a [positions, rope_dim / 2, 2] table")
-    table = _exact_tensor("rope", rope, rope.shape, torch.float32, device)
-    return wq, wk, w32, table, rope.shape[0], 2 * rope.shape[1]
-
-
-class _Place:
-    """Makes a call's device current and, with a stream of the caller's,
-    allocates on it; entering gives the stream's handle.  A single token's call
-    is bound by the host, and torch.cuda.device and current_stream take 4 us of
-    it, so the device is only switched where it differs and the current
-    stream's handle is asked for directly (0.1 us)."""
-    __slots__ = ("guards", "raw")
-
-    def __init__(self, device, stream):
-        self.guards = ()
-        if torch.cuda.current_device() != device.index:
-            self.guards = (torch.cuda.device(device),)
-        if stream is None:
-            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream: expected device {device}, got {stream.device}")
-            self.guards += (torch.cuda.stream(stream),)
-            self.raw = stream.cuda_stream
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _call(function, stream, t, *args):
+    """function(*args) on the caller's stream, or on the current one of t's device."""
+    if stream is None:
+        return function(*args)
+    with _on(stream, t.device):
+        return function(*args)
 
 
 def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cuda", stream=None):
@@ -628,10 +578,12 @@ def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cud
         raise ValueError("device: expected a CUDA device")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    with _Place(device, stream) as s:
+    stream = stream or torch.cuda.current_stream(device)
+    with torch.cuda.device(device), _on(stream, device):
         table = torch.empty((max(0, int(positions)), max(0, rope_dim) // 2, 2),
                             dtype=torch.float32, device=device)
-        _check(fa_rope_table(table.data_ptr(), positions, rope_dim, base, s), "fa_rope_table")
+        _check(fa_rope_table(table.data_ptr(), positions, rope_dim, base, stream.cuda_stream),
+               "fa_rope_table")
     return table
 
 
@@ -644,35 +596,8 @@ def qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-6, 
     projection): RMS norm of each row with the weights (both or neither, bf16
     or fp32) and rotation by the table ``rope`` (see ``rope_table``) at
     ``positions`` [B,N] int32 (default: 0 .. N-1)."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("expected [B, N, H, d] tensors")
-    device = _require_cuda("q", q)
-    B, N, Hq, d = q.shape
-    Hkv = k.shape[2]
-    strides = _rows("q", q, q.shape, device) + _rows("k", k, (B, N, Hkv, d), device)
-    if v is not None:
-        strides += _rows("v", v, (B, N, Hkv, d), device)
-    elif v_out is not None:
-        raise ValueError("v_out without v")
-    wq, wk, w32, table, rows, width = _norm_rope_args(q_weight, k_weight, rope, d, device)
-    pos = 0
-    if positions is not None:
-        pos = _exact_tensor("positions", positions, (B, N), torch.int32, device)
-    with _Place(device, stream) as s:
-        if q_out is None:
-            q_out = q.new_empty((B, Hq, N, d))
-        if k_out is None:
-            k_out = q.new_empty((B, Hkv, N, d))
-        if v is not None and v_out is None:
-            v_out = q.new_empty((B, Hkv, N, d))
-        _check(fa_qk_norm_rope(
-            q.data_ptr(), k.data_ptr(), v.data_ptr() if v is not None else 0, strides, wq, wk,
-            w32, eps, table, rows, width, int(interleaved), pos,
-            _exact_tensor("q_out", q_out, (B, Hq, N, d), torch.bfloat16, device),
-            _exact_tensor("k_out", k_out, (B, Hkv, N, d), torch.bfloat16, device),
-            _exact_tensor("v_out", v_out, (B, Hkv, N, d), torch.bfloat16, device)
-            if v is not None else 0, B, N, Hq, Hkv, d, s), "fa_qk_norm_rope")
-    return q_out, k_out, v_out
+    return _call(_native().qk_norm_rope, stream, q, q, k, v, q_weight, k_weight, eps, rope,
+                 positions, interleaved, q_out, k_out, v_out)
 
 
 def qk_norm_rope_backward(dq_out, dk_out, dv_out, q, k, q_weight=None, k_weight=None,
@@ -685,70 +610,8 @@ def qk_norm_rope_backward(dq_out, dk_out, dv_out, q, k, q_weight=None, k_weight=
     strides whose rows do not overlap (such as parts of one packed gradient;
     default: contiguous); the weights' gradients are [d] fp32, None without
     weights (q and k are then not read and may be None)."""
-    if dq_out.dim() != 4 or dk_out.dim() != 4:
-        raise ValueError("expected [B, H, N, d] gradients")
-    device = _require_cuda("dq_out", dq_out)
-    B, Hq, N, d = dq_out.shape
-    Hkv = dk_out.shape[1]
-    qs, ks = (B, N, Hq, d), (B, N, Hkv, d)
-    gq = _exact_tensor("dq_out", dq_out, (B, Hq, N, d), torch.bfloat16, device)
-    gk = _exact_tensor("dk_out", dk_out, (B, Hkv, N, d), torch.bfloat16, device)
-    gv = 0
-    if dv_out is not None:
-        gv = _exact_tensor("dv_out", dv_out, (B, Hkv, N, d), torch.bfloat16, device)
-    elif dv is not None:
-        raise ValueError("dv without dv_out")
-    wq, wk, w32, table, rows, width = _norm_rope_args(q_weight, k_weight, rope, d, device)
-    strides = None
-    if wq:
-        if q is None or k is None:
-            raise ValueError("q and k are needed for the gradients of a norm")
-        strides = _rows("q", q, qs, device) + _rows("k", k, ks, device)
-    pos = 0
-    if positions is not None:
-        pos = _exact_tensor("positions", positions, (B, N), torch.int32, device)
-    with _Place(device, stream) as s:
-        if dq is None:
-            dq = dq_out.new_empty(qs)
-        if dk is None:
-            dk = dq_out.new_empty(ks)
-        if dv is None and dv_out is not None:
-            dv = dq_out.new_empty(ks)
-        grads = _rows("dq", dq, qs, device) + _rows("dk", dk, ks, device)
-        if dv is not None:
-            grads += _rows("dv", dv, ks, device)
-        dwq = dwk = None
-        if wq:
-            dwq = dq_out.new_empty(d, dtype=torch.float32)
-            dwk = dq_out.new_empty(d, dtype=torch.float32)
-            if workspace is None:
-                workspace = dq_out.new_empty(max(1, fa_qk_norm_rope_bwd_workspace_size(d)),
-                                             dtype=torch.uint8)
-        ws, ws_bytes = _workspace(workspace, device)
-        _check(fa_qk_norm_rope_bwd(
-            gq, gk, gv, q.data_ptr() if wq else 0, k.data_ptr() if wq else 0, strides, wq, wk,
-            w32, eps, table, rows, width, int(interleaved), pos, dq.data_ptr(), dk.data_ptr(),
-            dv.data_ptr() if dv is not None else 0, grads, dwq.data_ptr() if wq else 0,
-            dwk.data_ptr() if wq else 0, B, N, Hq, Hkv, d, ws, ws_bytes, s),
-            "fa_qk_norm_rope_bwd")
-    return dq, dk, dv, dwq, dwk
-
-
-def _workspace(workspace, device):
-    """(pointer, bytes) of a workspace tensor, (0, 0) without one."""
-    if workspace is None:
-        return 0, 0
-    if workspace.device != device:
-        raise ValueError(f"workspace: expected device {device}, got {workspace.device}")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _cache_shape(k_pages, device):
-    if k_pages.dim() != 4:
-        raise ValueError("k_pages: expected [num_pages, Hkv, page_size, d]")
-    return tuple(k_pages.shape)
+    return _call(_native().qk_norm_rope_backward, stream, dq_out, dq_out, dk_out, dv_out, q, k,
+                 q_weight, k_weight, eps, rope, positions, interleaved, dq, dk, dv, workspace)
 
 
 def paged_append(q, k, v, k_pages, v_pages, block_table, seq_start, cache_len, rope=None,
@@ -762,35 +625,9 @@ def paged_append(q, k, v, k_pages, v_pages, block_table, seq_start, cache_len, r
     pos_offset + key index.  ``seq_start`` [S+1] holds each sequence's first
     token; all three are int32.  Rows of q_out that belong to no sequence are
     not written."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("expected [T, H, d] tensors")
-    device = _require_cuda("q", q)
-    T, Hq, d = q.shape
-    Hkv = k.shape[1]
-    strides = _rows("q", q, q.shape, device) + _rows("k", k, (T, Hkv, d), device) \
-        + _rows("v", v, (T, Hkv, d), device)
-    pages, heads, page_size, _ = shape = _cache_shape(k_pages, device)
-    if heads != Hkv:
-        raise ValueError(f"k_pages: expected {Hkv} heads, got {heads}")
-    if block_table.dim() != 2:
-        raise ValueError("block_table: expected [S, max_pages]")
-    S, max_pages = block_table.shape
-    kp = _exact_tensor("k_pages", k_pages, (pages, Hkv, page_size, d), torch.bfloat16, device)
-    vp = _exact_tensor("v_pages", v_pages, shape, torch.bfloat16, device)
-    bt = _exact_tensor("block_table", block_table, (S, max_pages), torch.int32, device)
-    ss = _exact_tensor("seq_start", seq_start, (S + 1,), torch.int32, device)
-    cl = _exact_tensor("cache_len", cache_len, (S,), torch.int32, device)
-    wq, wk, w32, table, rows, width = _norm_rope_args(q_weight, k_weight, rope, d, device)
-    with _Place(device, stream) as s:
-        if q_out is None:
-            q_out = q.new_empty((T, Hq, d))
-        qo = _exact_tensor("q_out", q_out, (T, Hq, d), torch.bfloat16, device)
-        if T:
-            _check(fa_paged_append(
-                q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, wq, wk, w32, eps, table, rows,
-                width, int(interleaved), pos_offset, ss, cl, bt, qo, kp, vp, S, T, Hq, Hkv, d,
-                page_size, pages, max_pages, s), "fa_paged_append")
-    return q_out
+    return _call(_native().paged_append, stream, q, q, k, v, k_pages, v_pages, block_table,
+                 seq_start, cache_len, rope, pos_offset, q_weight, k_weight, eps, interleaved,
+                 q_out)
 
 
 def attention_paged(q, k_pages, v_pages, block_table, seq_start, kv_len, scale: float,
@@ -805,45 +642,5 @@ def attention_paged(q, k_pages, v_pages, block_table, seq_start, kv_len, scale: 
     three are int32.  max_new: the most new tokens any sequence has (default:
     T, which launches more work than a tight bound).  Rows that belong to no
     sequence are not written."""
-    if q.dim() != 3:
-        raise ValueError("expected q [T, Hq, d]")
-    device = _require_cuda("q", q)
-    T, Hq, d = q.shape
-    qp = _exact_tensor("q", q, q.shape, torch.bfloat16, device)
-    pages, Hkv, page_size, _ = shape = _cache_shape(k_pages, device)
-    if block_table.dim() != 2:
-        raise ValueError("block_table: expected [S, max_pages]")
-    S, max_pages = block_table.shape
-    kp = _exact_tensor("k_pages", k_pages, (pages, Hkv, page_size, d), torch.bfloat16, device)
-    vp = _exact_tensor("v_pages", v_pages, shape, torch.bfloat16, device)
-    bt = _exact_tensor("block_table", block_table, (S, max_pages), torch.int32, device)
-    ss = _exact_tensor("seq_start", seq_start, (S + 1,), torch.int32, device)
-    kl = _exact_tensor("kv_len", kv_len, (S,), torch.int32, device)
-    pp = 0
-    if prefix_len:
-        if prefix_pages is None:
-            raise ValueError("prefix_len without prefix_pages")
-        if page_size and prefix_pages.numel() * page_size < prefix_len:
-            raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages do not hold "
-                             f"{prefix_len} keys")
-        pp = _exact_tensor("prefix_pages", prefix_pages, (prefix_pages.numel(),), torch.int32,
-                           device)
-    most = T if max_new is None else int(max_new)
-    with _Place(device, stream) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = q.new_empty((T, Hq), dtype=torch.float32)
-        op = _exact_tensor("out", out, (T, Hq, d), torch.bfloat16, device)
-        lp = _exact_tensor("lse", lse, (T, Hq), torch.float32, device)
-        if T:
-            if workspace is None:
-                need = fa_paged_workspace_size(S, T, Hq, Hkv, d, page_size, max_pages,
-                                               prefix_len, most)
-                if need:
-                    workspace = q.new_empty(need, dtype=torch.uint8)
-            ws, ws_bytes = _workspace(workspace, device)
-            _check(fa_fwd_paged(qp, kp, vp, bt, ss, kl, pp, prefix_len, op, lp, S, T, Hq, Hkv, d,
-                                page_size, pages, max_pages, most, scale, ws, ws_bytes, s),
-                   "fa_fwd_paged")
-    return out, lse
+    return _call(_native().attention_paged, stream, q, q, k_pages, v_pages, block_table,
+                 seq_start, kv_len, scale, prefix_pages, prefix_len, max_new, out, lse, workspace)

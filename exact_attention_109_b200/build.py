@@ -1,9 +1,11 @@
-"""Build libfa_sm100.so in-tree with nvcc for sm_100a."""
+"""Build libfa_sm100.so in-tree with nvcc for sm_100a, and the compiled part of
+the Python binding with g++."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +24,8 @@ def headers():
     return out
 
 OUT = os.path.join(HERE, "libfa_sm100.so")
+BINDING_SOURCE = os.path.join(HERE, "csrc", "fa_binding.cpp")
+BINDING = os.path.join(HERE, "_fa_binding.so")
 
 
 def nvcc_command(out: str = OUT, extra=()):
@@ -31,20 +35,38 @@ def nvcc_command(out: str = OUT, extra=()):
             "-I", os.path.join(ROOT, "include"), "-o", out, *SOURCES, *extra]
 
 
-def up_to_date(out: str = OUT) -> bool:
+def binding_command(out: str = BINDING):
+    """The compiled part of the Python binding, against this torch's headers."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    flags = []
+    for p in include_paths(device_type="cuda") + [sysconfig.get_paths()["include"]]:
+        flags += ["-isystem", p]
+    for p in library_paths(device_type="cuda"):
+        flags += ["-L", p]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", os.path.join(ROOT, "include"), *flags, "-o", out, BINDING_SOURCE,
+            "-L", HERE, "-l:" + os.path.basename(OUT), "-Wl,-rpath,$ORIGIN",
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+
+
+def up_to_date(out: str = OUT, sources=None) -> bool:
     if not os.path.exists(out):
         return False
     t = os.path.getmtime(out)
-    return all(os.path.getmtime(f) <= t for f in SOURCES + headers())
+    return all(os.path.getmtime(f) <= t for f in (sources or SOURCES + headers()))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or not up_to_date():
         extra = ["-Xptxas", "-v"] if verbose else []
         subprocess.run(nvcc_command(extra=extra), check=True)
+    if force or not up_to_date(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h")]):
+        subprocess.run(binding_command(), check=True)
     return OUT
 
 
 if __name__ == "__main__":
-    build(force=True, verbose="-v" in sys.argv)
+    build(force="--changed" not in sys.argv, verbose="-v" in sys.argv)
     print(OUT)

@@ -236,8 +236,9 @@ def check_backward(c, dy, interleaved, grad, dwq, dwk):
         if w is None:
             assert dw is None
             continue
-        # A thread adds at most one row of every head of each token block its
-        # CTA walks (592 CTAs), then 40 sums over lanes, warps and CTAs.
+        # A thread adds at most one row of every head of each token block (of
+        # 16 or 32) its CTA walks (up to 296 CTAs) and of one more, then 40
+        # sums over lanes, warps and CTAs.
         chain = x.shape[2] * (-(-(B * N) // (8 * 592)) + 1) + 40
         ref.check(dw, want_w, (32 + chain) * ref.U * mag)
     assert torch.equal(dv, dy[2].transpose(1, 2))

@@ -773,14 +773,20 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     long long rem, quota;
     const bool any = line_start<T::THREADS>(p, reinterpret_cast<long long*>(smem + T::SCAN_OFF),
                                             s0, rem, quota);
+    // The merge waits for this grid only, so this grid ends after the prefix
+    // grid (which it was allowed to overtake): its first CTA waits for that, at
+    // its end, and keeps no other from its place.
+    auto leave = [] {
+        if (blockIdx.x == 0) grid_dependency_wait();
+    };
     if (!any) {
-        grid_dependency_wait();
+        leave();
         return;
     }
     const AbortState st{abort_flag, p.err};
     LineWalk walk(p, s0, rem, quota);
     if (walk.empty() && !walk.next(p)) {
-        grid_dependency_wait();
+        leave();
         return;
     }
 
@@ -823,7 +829,7 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
         // Do not leave with copies in flight.
         for (int j = max(0, issued - T::NSTAGE); j < issued; ++j)
             mbar_wait_bounded(&full[j % T::NSTAGE], (j / T::NSTAGE) & 1);
-        grid_dependency_wait();
+        leave();
         return;
     }
 
@@ -1066,9 +1072,7 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[slot]);
     } while (ok && walk.next(p));
-    // The merge waits for this grid only, so this grid ends after the prefix
-    // grid (which it was allowed to overtake).
-    grid_dependency_wait();
+    leave();
 }
 
 // ------------------------------------------------------------------ merge

@@ -18,8 +18,9 @@ using fa_host::aligned;
 // that an SM's registers hold, on each of 148 SMs.
 constexpr int kBwdCtas = 296;
 constexpr long long kMinHeads = 2;  // heads that a CTA takes at least
-// CTAs below which the heads of a token block are spread over more CTAs.
-constexpr long long kWantCtas = 592;
+// CTAs up to which the heads of a token block are spread over more CTAs: three
+// on each of 148 SMs, one wave.
+constexpr long long kWantCtas = 444;
 constexpr int kHeadsPerCta = 16;
 
 // Strides (in elements) of one input tensor: 16-byte rows, no negative step.
@@ -95,7 +96,7 @@ fa::RopeParams rope_params(const void* wq, const void* wk, int w_f32, float eps,
 // 10 (the set-up of a CTA counts).
 int head_groups(long long blocks, int heads) {
     const long long g =
-        std::max<long long>((kWantCtas + blocks - 1) / blocks, heads / kHeadsPerCta);
+        std::max<long long>(kWantCtas / blocks, heads / kHeadsPerCta);
     return static_cast<int>(std::max(1ll, std::min<long long>(g, heads)));
 }
 

@@ -18,8 +18,18 @@ constexpr int kMaxDevices = 64;
 // CTAs at most: they bound the workspace.
 constexpr long long kMaxPrefixCtas = 512;
 constexpr int kMaxLineCtas = 444;
-// Query rows of a key head for which the prefix joins the line of the sequences.
+// Query rows of a key head for which the prefix joins the line of the sequences:
+// one row tile, so that its keys are still read once, and a launch less.  16
+// sequences, 8 heads of 64, behind 1024 / 4096 / 65536 keys: 12.7 / 14.8 /
+// 43.7 us in the line, 17.1 / 19.4 / 46.7 on the tensor-core path; heads of 128
+// 16.7 / 20.1 / 71.5 against 21.0 / 24.5 / 69.7.  32 rows: 44.9 in the line
+// against 39.8 (16384 keys of 128).
 constexpr int kLinePrefixRows = 16;
+// Output rows up to which the merge takes four warps for each: few rows may have
+// many pieces, many rows fill the GPU anyway.  32 rows behind 16384 keys: 22 us
+// with four, 34 with one; 16 rows behind 1024: 12.3 and 14.2; 2048 rows with 17
+// pieces each: 73 and 69.
+constexpr long long kWideMergeRows = 1024;
 
 struct Plan {
     int tiles;            // query tiles per prefix CTA
@@ -180,7 +190,9 @@ cudaError_t launch_all(const Plan& pl, const CUtensorMap& mk, const CUtensorMap&
                fa::OwnTraits<D>::SMEM_BYTES, prefix, s, mk, mv, prm);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(prm.T) * prm.Hq;
-    return launch(fa::fa_paged_merge_kernel<D>, (rows + 3) / 4, 128, 0, true, s, prm);
+    return rows <= kWideMergeRows
+               ? launch(fa::fa_paged_merge_kernel<D, 4>, rows, 128, 0, true, s, prm)
+               : launch(fa::fa_paged_merge_kernel<D, 1>, (rows + 3) / 4, 128, 0, true, s, prm);
 }
 
 }  // namespace

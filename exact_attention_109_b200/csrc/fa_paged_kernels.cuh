@@ -1085,6 +1085,16 @@ struct RowSum {
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = 0.f;
     }
+    // Adds another sum, of the same values of the row.
+    __device__ __forceinline__ void join(float M2, float L2, const float (&v)[PER]) {
+        const float M1 = fmaxf(M, M2);
+        const float f = M == M1 ? 1.f : ex2_approx(M - M1);
+        const float f2 = M2 == M1 ? 1.f : ex2_approx(M2 - M1);
+        M = M1;
+        L = L * f + L2 * f2;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = acc[i] * f + v[i] * f2;
+    }
     // Adds up to U partial results: O values in v, and lane x's log-sum-exp of
     // the x-th in ls.  One with nothing seen (-inf) has weight 0, and its O was
     // never written.
@@ -1111,16 +1121,18 @@ struct RowSum {
     }
 };
 
-// One warp per output row (token, query head): with w_x = 2^(lse_x - M) over
+// W warps per output row (token, query head): with w_x = 2^(lse_x - M) over
 // the row's partial results, O = sum_x w_x O_x / sum_x w_x.  What this costs is
 // its chain of dependent reads, so the prefix's first splits, whose places are
 // known, are read at once with the row's table entry, and its first pieces
-// before any of them is added up.
-template <int D>
+// before any of them is added up.  Few rows may have many pieces (a long
+// sequence spread over the whole GPU): the row's warps take them in turn.
+template <int D, int W>
 __global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParams p) {
     constexpr int PER = D / 32, U = 8, V = 4;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
+    __shared__ float other[W > 1 ? W - 1 : 1][2 + PER][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
+    const long long row = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
     const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - 1ll * t * p.Hq);
     const int head = hq / p.G, g = hq - head * p.G;
     const bool mine = row < static_cast<long long>(p.T) * p.Hq && t >= p.seq_start[0] &&
@@ -1180,16 +1192,33 @@ __global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParam
     };
     RowSum<PER> sum;
     float splits[U][PER], pieces[V][PER];
-    float split_ls = load_splits(0, splits);
+    float split_ls = load_splits(U * part, splits);
     if (p.prefix_len == 0 && own.x == 1) return;  // written by its CTA
-    float piece_ls = load_pieces(0, pieces);
-    for (int x = 0; x < p.prefix_splits;) {
+    float piece_ls = load_pieces(V * part, pieces);
+    for (int x = U * part; x < p.prefix_splits;) {
         sum.add(splits, split_ls);
-        if ((x += U) < p.prefix_splits) split_ls = load_splits(x, splits);
+        if ((x += U * W) < p.prefix_splits) split_ls = load_splits(x, splits);
     }
-    for (int x = 0; x < pre.x + own.x;) {
+    for (int x = V * part; x < pre.x + own.x;) {
         sum.add(pieces, piece_ls);
-        if ((x += V) < pre.x + own.x) piece_ls = load_pieces(x, pieces);
+        if ((x += V * W) < pre.x + own.x) piece_ls = load_pieces(x, pieces);
+    }
+    if constexpr (W > 1) {  // the whole block is one row's
+        if (part > 0) {
+            other[part - 1][0][lane] = sum.M;
+            other[part - 1][1][lane] = sum.L;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) other[part - 1][2 + i][lane] = sum.acc[i];
+        }
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w) {
+            float v[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) v[i] = other[w][2 + i][lane];
+            sum.join(other[w][0][lane], other[w][1][lane], v);
+        }
     }
     const bool none = sum.L == 0.f;
     const float inv = none ? 0.f : 1.f / sum.L;

@@ -122,6 +122,14 @@ struct PrefixTraits {
 // have two TMEM buffers, so that the tensor core computes the next block's
 // while the softmax works on this one's; with two tiles each has its own and
 // they alternate.  TMEM columns: scores / P at 0 and 128, O at 256 (+ D).
+//
+// Measured with two tiles and heads of 128: 1.83 us a block of 128 keys for 256
+// rows, 1.36 PFLOP/s over 144 CTAs (84 % of the measured bf16 peak), bound by a
+// tile's chain of score product, softmax and value product; set-up 4 us, the
+// partial results 3 us.  1024 rows behind 65536 keys of 4 heads: 113 to 125 us.
+// One tile, heads of 64: 1.05 us a block, the softmax of the warps that have
+// rows.  Moving exponentials to the FMA pipes or handing P over in halves
+// changed nothing or made it slower.
 template <int D, int TILES>
 __global__ void __launch_bounds__(128 * (TILES + 1), 1)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -738,6 +746,15 @@ __device__ __forceinline__ void add_visible(const uint8_t* v, int r, int col,
 // head r % G of its new token r / G.  Each of four warps takes 16 keys of every
 // 64-key stage and keeps its own running maximum, sum and O; they are merged
 // at the end of a tile's share.
+//
+// Bound by HBM: with 4 * D bytes a key against 16 rows the mma.sync tiles need
+// less time than the reads (a 64-key stage of 128 takes 1.25 us of a CTA's
+// chain, its share of HBM 1.46 us with two CTAs an SM).  16 sequences of 8192
+// keys, 16 heads of 128: 169 to 184 us for 1.07 GB (89 to 97 % of the measured
+// copy bandwidth).  Ragged short sequences pay the first 6 us, in which the
+// lengths, page table and first stages come in one after another, and 3.3 us a
+// tile beside its keys: 64 sequences of 512 keys on average, 8 heads of 128:
+// 39 us for 134 MB.
 template <int D>
 __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     fa_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -763,11 +780,14 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    // Lengths and counts out of range are reported once.
+    // Starts, lengths and counts out of range are reported once.
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.S; i += T::THREADS) {
             const LineSeq q(p, i);
-            if (q.n > 0 && (p.kv_len[i] != q.len || q.n > p.max_new)) atomicOr(p.err, kErrIndex);
+            const int a = p.seq_start[i], z = p.seq_start[i + 1];
+            if (a < 0 || z < a || z > p.T ||
+                (q.n > 0 && (p.kv_len[i] != q.len || q.n > p.max_new)))
+                atomicOr(p.err, kErrIndex);
         }
     int s0;
     long long rem, quota;
@@ -843,234 +863,236 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     int done = 0;  // stages read so far
     bool ok = true, first = true;
     do {
-    const LineSeq& seq = walk.seq;
-    const int start = seq.start, n = seq.n, len = seq.len, head = walk.head;
-    const int rows = n * p.G, r0 = walk.rt * T::ROWS;
-    const bool prefix = walk.s == p.S;
-    const int2 keys = walk.keys(p);
-    const int kbeg = keys.x, kend = keys.y, nblk = (kend - kbeg + T::BK - 1) / T::BK;
-    // Row r of the tile: its output row, and its row among the partials.
-    auto out_row = [&](int r) {
-        const int i = (r0 + r) / p.G;
-        return static_cast<long long>(start + i) * p.Hq + head * p.G + (r0 + r - i * p.G);
-    };
-    const bool whole = walk.whole();
-    const bool direct = whole && p.prefix_len == 0;
-    const long long part0 =
-        whole ? (static_cast<long long>(prefix ? 0 : p.slots - 1) * p.Hkv + head) * p.R +
-                    static_cast<long long>(start) * p.G + r0
-              : p.piece_row + (2ll * blockIdx.x + (first ? 0 : 1)) * T::ROWS;
-    if (walk.b0 == 0 && threadIdx.x < T::ROWS && r0 + static_cast<int>(threadIdx.x) < rows) {
-        // The tile's later blocks are the next CTAs', `quota` for each.
-        const int rest = seq.blocks - walk.b1;
-        const int2 d = make_int2(
-            rest <= 0 ? 1 : 2 + static_cast<int>(quotient(rest - 1, quota)),
-            (2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1)) * T::ROWS + threadIdx.x);
-        p.pieces[(static_cast<long long>(prefix) * p.Hkv + head) * p.R +
-                 static_cast<long long>(start) * p.G + r0 + threadIdx.x] = d;
-    }
-    first = false;
-    if (nblk == 0) {
-        // No key in this share: an empty partial, or the empty row's result.
-        for (int i = threadIdx.x; i < T::ROWS * (D / 8); i += T::NCW * 32) {
-            const int r = i / (D / 8), u = i % (D / 8);
-            if (r0 + r >= rows) break;  // i rises with r
-            if (direct)
-                *reinterpret_cast<uint4*>(p.o + out_row(r) * D + 8 * u) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            if (u == 0) (direct ? p.lse[out_row(r)] : p.part_lse[part0 + r]) = -INFINITY;
+        const LineSeq& seq = walk.seq;
+        const int start = seq.start, n = seq.n, len = seq.len, head = walk.head;
+        const int rows = n * p.G, r0 = walk.rt * T::ROWS;
+        const bool prefix = walk.s == p.S;
+        const int2 keys = walk.keys(p);
+        const int kbeg = keys.x, kend = keys.y, nblk = (kend - kbeg + T::BK - 1) / T::BK;
+        // Row r of the tile: its output row, and its row among the partials.
+        auto out_row = [&](int r) {
+            const int i = (r0 + r) / p.G;
+            return static_cast<long long>(start + i) * p.Hq + head * p.G + (r0 + r - i * p.G);
+        };
+        const bool whole = walk.whole();
+        const bool direct = whole && p.prefix_len == 0;
+        const long long part0 =
+            whole ? (static_cast<long long>(prefix ? 0 : p.slots - 1) * p.Hkv + head) * p.R +
+                        static_cast<long long>(start) * p.G + r0
+                  : p.piece_row + (2ll * blockIdx.x + (first ? 0 : 1)) * T::ROWS;
+        if (walk.b0 == 0 && threadIdx.x < T::ROWS && r0 + static_cast<int>(threadIdx.x) < rows) {
+            // The tile's later blocks are the next CTAs', `quota` for each.
+            const int rest = seq.blocks - walk.b1;
+            const int2 d = make_int2(
+                rest <= 0 ? 1 : 2 + static_cast<int>(quotient(rest - 1, quota)),
+                (2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1)) * T::ROWS + threadIdx.x);
+            p.pieces[(static_cast<long long>(prefix) * p.Hkv + head) * p.R +
+                     static_cast<long long>(start) * p.G + r0 + threadIdx.x] = d;
         }
-        continue;
-    }
-    uint32_t qa[D / 16][4];
-    int lim[2];  // last visible key of rows rq and rq + 8
-    const int lim0 = prefix ? len : len - n + r0 / p.G;  // and of the tile's first row
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int r = r0 + rq + 8 * x;
-        lim[x] = r >= rows ? -1 : prefix ? len - 1 : min(len, len - n + r / p.G + 1) - 1;
-        const __nv_bfloat16* src = p.q + (r < rows ? out_row(rq + 8 * x) : 0) * D + 2 * cq;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            qa[k][x] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
-            qa[k][x + 2] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+        first = false;
+        if (nblk == 0) {
+            // No key in this share: an empty partial, or the empty row's result.
+            for (int i = threadIdx.x; i < T::ROWS * (D / 8); i += T::NCW * 32) {
+                const int r = i / (D / 8), u = i % (D / 8);
+                if (r0 + r >= rows) break;  // i rises with r
+                if (direct)
+                    *reinterpret_cast<uint4*>(p.o + out_row(r) * D + 8 * u) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                if (u == 0) (direct ? p.lse[out_row(r)] : p.part_lse[part0 + r]) = -INFINITY;
+            }
+            continue;
         }
-    }
-    float o[D / 8][4];
+        uint32_t qa[D / 16][4];
+        int lim[2];  // last visible key of rows rq and rq + 8
+        const int lim0 = prefix ? len : len - n + r0 / p.G;  // and of the tile's first row
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
-
-    int slot = 0;
-    for (int j = 0; j < nblk; ++j, ++done) {
-        slot = done % T::NSTAGE;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (done / T::NSTAGE) & 1, st));
-        if (!ok) break;
-        const uint32_t kt = smem_u32(smem + slot * T::STAGE_BYTES);
-        const int j0 = kbeg + j * T::BK + 16 * warp;  // the warp's first key
-        if (j0 < kend) {
-            float sc[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+        for (int x = 0; x < 2; ++x) {
+            const int r = r0 + rq + 8 * x;
+            lim[x] = r >= rows ? -1 : prefix ? len - 1 : min(len, len - n + r / p.G + 1) - 1;
+            const __nv_bfloat16* src = p.q + (r < rows ? out_row(rq + 8 * x) : 0) * D + 2 * cq;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                const int u = 2 * k + unit_k;
-                uint32_t b[4];
-                ldsm4(kt + (u >> 3) * T::CHUNK_BYTES + sw128_offset(key_k, u & 7), b);
-                mma16816(sc[0], qa[k], b[0], b[1]);
-                mma16816(sc[1], qa[k], b[2], b[3]);
+                qa[k][x] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+                qa[k][x + 2] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
             }
-            // Online softmax of rows rq and rq + 8 over the warp's 16 keys.
-            uint32_t pa[4];
+        }
+        float o[D / 8][4];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float v[4];
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
+
+        int slot = 0;
+        for (int j = 0; j < nblk; ++j, ++done) {
+            slot = done % T::NSTAGE;
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (done / T::NSTAGE) & 1, st));
+            if (!ok) break;
+            const uint32_t kt = smem_u32(smem + slot * T::STAGE_BYTES);
+            const int j0 = kbeg + j * T::BK + 16 * warp;  // the warp's first key
+            if (j0 < kend) {
+                float sc[2][4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = j0 + 8 * i + 2 * cq + e;
-                        v[2 * i + e] = key < kend && key <= lim[x]
-                                           ? sc[i][2 * x + e] * p.scale_log2
-                                           : -INFINITY;
+                    for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int u = 2 * k + unit_k;
+                    uint32_t b[4];
+                    ldsm4(kt + (u >> 3) * T::CHUNK_BYTES + sw128_offset(key_k, u & 7), b);
+                    mma16816(sc[0], qa[k], b[0], b[1]);
+                    mma16816(sc[1], qa[k], b[2], b[3]);
+                }
+                // Online softmax of rows rq and rq + 8 over the warp's 16 keys.
+                uint32_t pa[4];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = j0 + 8 * i + 2 * cq + e;
+                            v[2 * i + e] = key < kend && key <= lim[x]
+                                               ? sc[i][2 * x + e] * p.scale_log2
+                                               : -INFINITY;
+                        }
+                    float bm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                    if (bm > m[x] + 8.f) {
+                        const float alpha = ex2_approx(m[x] - bm);  // 0 while m = -inf
+                        l[x] *= alpha;
+                        lr[x] *= alpha;
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            o[i][2 * x] *= alpha;
+                            o[i][2 * x + 1] *= alpha;
+                        }
+                        m[x] = bm;
                     }
-                float bm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                if (bm > m[x] + 8.f) {
-                    const float alpha = ex2_approx(m[x] - bm);  // 0 while m = -inf
-                    l[x] *= alpha;
-                    lr[x] *= alpha;
+                    const float mm = m[x] == -INFINITY ? 0.f : m[x];
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        o[i][2 * x] *= alpha;
-                        o[i][2 * x + 1] *= alpha;
+                    for (int i = 0; i < 2; ++i) {
+                        const float p0 = ex2_approx(v[2 * i] - mm);
+                        const float p1 = ex2_approx(v[2 * i + 1] - mm);
+                        l[x] += p0 + p1;
+                        pa[2 * i + x] = pack_bf16x2(p0, p1);
+                        float a = 0.f, b = 0.f;
+                        add_bf16x2_to_f32(pa[2 * i + x], a, b);
+                        lr[x] += a + b;
                     }
-                    m[x] = bm;
                 }
-                const float mm = m[x] == -INFINITY ? 0.f : m[x];
+                // Keys 2cq, 2cq + 1 (b0) and 2cq + 8, 2cq + 9 (b1) behind the
+                // last one: their values count as zeros.
+                const int left = kend - j0;
+                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                if (left < 16) {
+                    keep0 = (2 * cq < left ? 0xffffu : 0u) | (2 * cq + 1 < left ? 0xffff0000u : 0u);
+                    keep1 = (2 * cq + 8 < left ? 0xffffu : 0u) |
+                            (2 * cq + 9 < left ? 0xffff0000u : 0u);
+                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float p0 = ex2_approx(v[2 * i] - mm), p1 = ex2_approx(v[2 * i + 1] - mm);
-                    l[x] += p0 + p1;
-                    pa[2 * i + x] = pack_bf16x2(p0, p1);
-                    float a = 0.f, b = 0.f;
-                    add_bf16x2_to_f32(pa[2 * i + x], a, b);
-                    lr[x] += a + b;
+                for (int i = 0; i < D / 16; ++i) {
+                    const int u = 2 * i + unit_v;
+                    uint32_t b[4];
+                    ldsm4t(kt + T::TILE_BYTES + (u >> 3) * T::CHUNK_BYTES +
+                               sw128_offset(key_v, u & 7),
+                           b);
+                    b[0] &= keep0;
+                    b[1] &= keep1;
+                    b[2] &= keep0;
+                    b[3] &= keep1;
+                    // A key that some rows do not see must not reach them, and a
+                    // weight of zero times infinity would: such values are added
+                    // row by row.
+                    if (j0 + 15 > lim0 &&
+                        __any_sync(0xffffffffu, not_finite(b[0]) || not_finite(b[1]) ||
+                                                    not_finite(b[2]) || not_finite(b[3]))) {
+                        add_visible<T::CHUNK_BYTES>(smem + slot * T::STAGE_BYTES + T::TILE_BYTES,
+                                                    16 * warp, 16 * i + 2 * cq, pa, lim, j0, kend,
+                                                    o[2 * i], o[2 * i + 1]);
+                        continue;
+                    }
+                    mma16816(o[2 * i], pa, b[0], b[1]);
+                    mma16816(o[2 * i + 1], pa, b[2], b[3]);
                 }
             }
-            // Keys 2cq, 2cq + 1 (b0) and 2cq + 8, 2cq + 9 (b1) behind the
-            // last one: their values count as zeros.
-            const int left = kend - j0;
-            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-            if (left < 16) {
-                keep0 = (2 * cq < left ? 0xffffu : 0u) | (2 * cq + 1 < left ? 0xffff0000u : 0u);
-                keep1 = (2 * cq + 8 < left ? 0xffffu : 0u) |
-                        (2 * cq + 9 < left ? 0xffff0000u : 0u);
-            }
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const int u = 2 * i + unit_v;
-                uint32_t b[4];
-                ldsm4t(kt + T::TILE_BYTES + (u >> 3) * T::CHUNK_BYTES + sw128_offset(key_v, u & 7),
-                       b);
-                b[0] &= keep0;
-                b[1] &= keep1;
-                b[2] &= keep0;
-                b[3] &= keep1;
-                // A key that some rows do not see must not reach them, and a
-                // weight of zero times infinity would: such values are added
-                // row by row.
-                if (j0 + 15 > lim0 &&
-                    __any_sync(0xffffffffu, not_finite(b[0]) || not_finite(b[1]) ||
-                                                not_finite(b[2]) || not_finite(b[3]))) {
-                    add_visible<T::CHUNK_BYTES>(smem + slot * T::STAGE_BYTES + T::TILE_BYTES,
-                                                16 * warp, 16 * i + 2 * cq, pa, lim, j0, kend,
-                                                o[2 * i], o[2 * i + 1]);
-                    continue;
-                }
-                mma16816(o[2 * i], pa, b[0], b[1]);
-                mma16816(o[2 * i + 1], pa, b[2], b[3]);
-            }
+            __syncwarp();
+            if (lane == 0 && j + 1 < nblk) mbar_arrive(&empty[slot]);
         }
-        __syncwarp();
-        if (lane == 0 && j + 1 < nblk) mbar_arrive(&empty[slot]);
-    }
 
-    // Row sums over the four lanes of a row, then the four warps' results
-    // through the tile's last stage, which is given back only after that.  Its
-    // 8-float units are swapped by row, so that the writes meet every bank.
+        // Row sums over the four lanes of a row, then the four warps' results
+        // through the tile's last stage, which is given back only after that.  Its
+        // 8-float units are swapped by row, so that the writes meet every bank.
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
-            lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], d);
+            for (int d = 1; d < 4; d <<= 1) {
+                l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
+                lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], d);
+            }
+        float* red = reinterpret_cast<float*>(smem + slot * T::STAGE_BYTES);  // [NCW][ROWS][D]
+        named_bar_sync(1, T::NCW * 32);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = warp * T::ROWS + rq + 8 * x;
+            if (cq == 0) {
+                red_ml[3 * r] = m[x];
+                red_ml[3 * r + 1] = l[x];
+                red_ml[3 * r + 2] = lr[x];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2*>(red + r * D + 8 * (i ^ (rq & 7)) + 2 * cq) =
+                    make_float2(o[i][2 * x], o[i][2 * x + 1]);
         }
-    float* red = reinterpret_cast<float*>(smem + slot * T::STAGE_BYTES);  // [NCW][ROWS][D]
-    named_bar_sync(1, T::NCW * 32);
+        // One answer for all warps, so that none waits here for one that gave up.
+        if (threadIdx.x == 0) *carry_on = *abort_flag == 0;
+        named_bar_sync(1, T::NCW * 32);
+        ok = *carry_on != 0;
+        for (int i = threadIdx.x; i < T::ROWS * (D / 4); i += T::NCW * 32) {
+            const int r = i / (D / 4), e4 = (i % (D / 4)) * 4;
+            if (r0 + r >= rows) break;  // i rises with r
+            float M = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int r = warp * T::ROWS + rq + 8 * x;
-        if (cq == 0) {
-            red_ml[3 * r] = m[x];
-            red_ml[3 * r + 1] = l[x];
-            red_ml[3 * r + 2] = lr[x];
+            for (int w = 0; w < T::NCW; ++w) M = fmaxf(M, red_ml[3 * (w * T::ROWS + r)]);
+            float L = 0.f, Lr = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < T::NCW; ++w) {
+                const float* ml = red_ml + 3 * (w * T::ROWS + r);
+                // A warp that saw nothing has l = O = 0; one whose scores were all
+                // NaN has m = -inf too, and its NaN must reach the row.
+                const float f = ml[0] == -INFINITY ? 1.f : ex2_approx(ml[0] - M);
+                const float4 x = *reinterpret_cast<const float4*>(
+                    red + (w * T::ROWS + r) * D + 8 * ((e4 >> 3) ^ (r & 7)) + (e4 & 7));
+                L += f * ml[1];
+                Lr += f * ml[2];
+                a.x += f * x.x;
+                a.y += f * x.y;
+                a.z += f * x.z;
+                a.w += f * x.w;
+            }
+            const bool none = L == 0.f;
+            const float inv = none ? 0.f : 1.f / Lr;
+            const float lse2 = none ? -INFINITY : M + log2f(L);
+            if (direct) {
+                uint2 w;
+                w.x = pack_bf16x2(a.x * inv, a.y * inv);
+                w.y = pack_bf16x2(a.z * inv, a.w * inv);
+                *reinterpret_cast<uint2*>(p.o + out_row(r) * D + e4) = w;
+                if (e4 == 0) p.lse[out_row(r)] = lse2 * 0.6931471805599453f;
+            } else {
+                *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + e4) =
+                    make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                if (e4 == 0) p.part_lse[part0 + r] = lse2;
+            }
         }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(red + r * D + 8 * (i ^ (rq & 7)) + 2 * cq) =
-                make_float2(o[i][2 * x], o[i][2 * x + 1]);
-    }
-    // One answer for all warps, so that none waits here for one that gave up.
-    if (threadIdx.x == 0) *carry_on = *abort_flag == 0;
-    named_bar_sync(1, T::NCW * 32);
-    ok = *carry_on != 0;
-    for (int i = threadIdx.x; i < T::ROWS * (D / 4); i += T::NCW * 32) {
-        const int r = i / (D / 4), e4 = (i % (D / 4)) * 4;
-        if (r0 + r >= rows) break;  // i rises with r
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < T::NCW; ++w) M = fmaxf(M, red_ml[3 * (w * T::ROWS + r)]);
-        float L = 0.f, Lr = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < T::NCW; ++w) {
-            const float* ml = red_ml + 3 * (w * T::ROWS + r);
-            // A warp that saw nothing has l = O = 0; one whose scores were all
-            // NaN has m = -inf too, and its NaN must reach the row.
-            const float f = ml[0] == -INFINITY ? 1.f : ex2_approx(ml[0] - M);
-            const float4 x = *reinterpret_cast<const float4*>(
-                red + (w * T::ROWS + r) * D + 8 * ((e4 >> 3) ^ (r & 7)) + (e4 & 7));
-            L += f * ml[1];
-            Lr += f * ml[2];
-            a.x += f * x.x;
-            a.y += f * x.y;
-            a.z += f * x.z;
-            a.w += f * x.w;
-        }
-        const bool none = L == 0.f;
-        const float inv = none ? 0.f : 1.f / Lr;
-        const float lse2 = none ? -INFINITY : M + log2f(L);
-        if (direct) {
-            uint2 w;
-            w.x = pack_bf16x2(a.x * inv, a.y * inv);
-            w.y = pack_bf16x2(a.z * inv, a.w * inv);
-            *reinterpret_cast<uint2*>(p.o + out_row(r) * D + e4) = w;
-            if (e4 == 0) p.lse[out_row(r)] = lse2 * 0.6931471805599453f;
-        } else {
-            *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + e4) =
-                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-            if (e4 == 0) p.part_lse[part0 + r] = lse2;
-        }
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[slot]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
     } while (ok && walk.next(p));
     leave();
 }
@@ -1123,7 +1145,8 @@ struct RowSum {
 
 // W warps per output row (token, query head): with w_x = 2^(lse_x - M) over
 // the row's partial results, O = sum_x w_x O_x / sum_x w_x.  What this costs is
-// its chain of dependent reads, so the prefix's first splits, whose places are
+// its chain of dependent reads (7 us for 2048 rows of 17 results, 18 MB, behind
+// the last CTA of the line), so the prefix's first splits, whose places are
 // known, are read at once with the row's table entry, and its first pieces
 // before any of them is added up.  Few rows may have many pieces (a long
 // sequence spread over the whole GPU): the row's warps take them in turn.

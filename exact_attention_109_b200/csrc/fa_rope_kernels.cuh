@@ -15,8 +15,15 @@
 // about ten fp32 operations.  So a row is held in registers by d / 8 lanes
 // (one 16-byte access each; 16 rows of 128 or 32 of 64 per CTA), its sums go
 // through shuffles, and everything that depends on the token alone (sequence,
-// page, angles) is read once and used for all heads the CTA walks.  All
-// arithmetic is fp32, rounded once on the way out.
+// page, angles) is read once and used for all heads the CTA walks.  Rows come
+// in through a ring of shared memory that each thread fills and reads for
+// itself.  All arithmetic is fp32, rounded once on the way out.
+//
+// Measured, 16384 tokens of 16 query, 16 key and 16 value heads of 128: forward
+// 69 us for 407 MB (90 % of the measured copy bandwidth; 87 us with the rows in
+// flight held in registers), backward 103 us for 541 MB (80 %; 191 us so).  The
+// forward's rest is the last wave; the backward issues in 70 % of its cycles
+// with the four warps a scheduler has room for.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -301,6 +308,11 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
             }
             if (page_row < 0) atomicOr(p.err, kErrIndex);
         }
+        if (blockIdx.x + blockIdx.y == 0)
+            for (int i = threadIdx.x; i < dst.S; i += kRopeThreads) {
+                const int a = dst.seq_start[i], z = dst.seq_start[i + 1];
+                if (a < 0 || z < a || z > p.N) atomicOr(p.err, kErrIndex);
+            }
     } else {
         pos = p.positions ? p.positions[row] : n;
     }

@@ -450,8 +450,9 @@ fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out,
  * sequence may have none; rows outside seq_start[0] .. seq_start[S]-1 belong
  * to nobody, and nothing is written for them.  Lengths, starts and pages are
  * device memory and are read by the kernels, so a captured graph follows their
- * values.  One that is out of range is reported as FA_ERR_INDEX by
- * fa_get_device_error; nothing outside the given buffers is touched.
+ * values.  One that is out of range (or starts that decrease) is reported as
+ * FA_ERR_INDEX by fa_get_device_error, and its sequence's rows are unspecified;
+ * nothing outside the given buffers is touched.
  *
  * fa_paged_append -- writes the new tokens' keys and values behind the rows
  * that a sequence has, with norm and rotation on the way (see above).

@@ -228,7 +228,7 @@ def test_loose_bound_and_workspace_reuse():
 
 @gpu
 @pytest.mark.parametrize("fault", ["page_high", "page_negative", "length_long", "length_negative",
-                                   "prefix_page", "many_new"])
+                                   "prefix_page", "many_new", "start_decreases", "start_late"])
 def test_bad_index_is_reported(fault):
     """A page, a length or a count out of range is reported; the other
     sequences' rows come out as before."""
@@ -247,13 +247,17 @@ def test_bad_index_is_reported(fault):
         bad["len"][1] = -5
     elif fault == "prefix_page":
         bad["prefix"][1] = 1 << 20
-    else:
-        bad["start"] = torch.tensor([0, 2, 4, 6], dtype=torch.int32)
+    elif fault == "many_new":
         kw["max_new"] = 1
+    elif fault == "start_decreases":
+        bad["start"] = torch.tensor([0, 4, 2, 6], dtype=torch.int32)
+        kw["max_new"] = 4
+    else:
+        bad["start"] = torch.tensor([0, 2, 4, 7], dtype=torch.int32)
     out, lse = run(bad, **kw)
     assert fa.fa_get_device_error() == fa.FA_ERR_INDEX
     assert fa.fa_get_device_error() == fa.FA_OK
-    if fault not in ("prefix_page", "many_new"):
+    if fault.startswith(("page", "length")):
         for a, b in ((out, good[0]), (lse, good[1])):
             assert torch.equal(a[:2], b[:2]) and torch.equal(a[4:], b[4:])
 

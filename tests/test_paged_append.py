@@ -138,7 +138,7 @@ def test_head_major_and_repeated_inputs():
 
 @gpu
 @pytest.mark.parametrize("fault", ["page_high", "page_negative", "table_short", "length_negative",
-                                   "length_huge", "position"])
+                                   "length_huge", "position", "start_decreases", "start_late"])
 def test_bad_index_is_reported_and_touches_nothing(fault):
     """A page, a length or a position out of range: the error is reported, the
     sequence's keys are not written, and everybody else's are."""
@@ -156,10 +156,16 @@ def test_bad_index_is_reported_and_touches_nothing(fault):
         bad["len"][1] = -3
     elif fault == "length_huge":
         bad["len"][1] = 2 ** 31 - 1
-    else:
+    elif fault == "position":
         bad["rope"] = c["rope"][:41]  # the third sequence's last position is 41
+    elif fault == "start_decreases":
+        bad["start"] = torch.tensor([0, 4, 2, 6], dtype=torch.int32)
+    else:
+        bad["start"] = torch.tensor([0, 2, 4, 7], dtype=torch.int32)
     out, kp, vp = run(bad)
     assert fa.fa_get_device_error() == fa.FA_ERR_INDEX
+    if fault.startswith("start"):
+        return
     if fault == "position":
         assert torch.equal(out[:5], good[0][:5]) and torch.equal(vp, good[2])
         return

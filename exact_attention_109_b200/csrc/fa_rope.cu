@@ -17,7 +17,10 @@ using fa_host::aligned;
 // CTAs of the backward kernel at most, and so rows of its dw partials: the two
 // that an SM's registers hold, on each of 148 SMs.
 constexpr int kBwdCtas = 296;
-constexpr long long kMinHeads = 2;  // heads that a CTA takes at least
+constexpr long long kMinHeads = 2;    // heads that a CTA takes at least
+constexpr long long kManyHeads = 16;  // from here on, twice as many CTAs take half each:
+                                      // the second wave evens out the first (16384 tokens of
+                                      // 48 heads of 128: 102 -> 100 us)
 // CTAs up to which the heads of a token block are spread over more CTAs: three
 // on each of 148 SMs, one wave.
 constexpr long long kWantCtas = 444;
@@ -133,14 +136,19 @@ cudaError_t launch_prep_bwd(const fa::HeadRows (&dy)[3], const fa::HeadRows (&x)
     const long long blocks = (static_cast<long long>(p.B) * p.N + TOKENS - 1) / TOKENS;
     const int heads = p.Hq + p.Hkv + (dy[2].p ? p.Hkv : 0);
     const long long units = blocks * heads;
-    const long long per_cta = std::max(kMinHeads, (units + kBwdCtas - 1) / kBwdCtas);
+    long long per_cta = std::max(kMinHeads, (units + kBwdCtas - 1) / kBwdCtas);
+    if (per_cta >= 2 * kManyHeads) per_cta = (per_cta + 1) / 2;
     const int grid = static_cast<int>((units + per_cta - 1) / per_cta);
-    fa::fa_prep_bwd_kernel<D, IL><<<grid, fa::kRopeThreads, 0, s>>>(
-        dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2], p, per_cta, part);
+    if (p.wq)
+        fa::fa_prep_bwd_kernel<D, IL, true><<<grid, fa::kRopeThreads, 0, s>>>(
+            dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2], p, per_cta, part);
+    else
+        fa::fa_prep_bwd_kernel<D, IL, false><<<grid, fa::kRopeThreads, 0, s>>>(
+            dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2], p, per_cta, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.wq) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * D / 32);
+    cfg.gridDim = dim3(2 * D / 8);
     cfg.blockDim = dim3(1024);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -220,7 +228,7 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v, const lon
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
-    return d == 64 || d == 128 ? static_cast<size_t>(kBwdCtas) * 2 * d * sizeof(float) : 0;
+    return d == 64 || d == 128 ? static_cast<size_t>(2 * kBwdCtas) * 2 * d * sizeof(float) : 0;
 }
 
 fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* dv_out,

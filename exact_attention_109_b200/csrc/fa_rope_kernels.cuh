@@ -20,10 +20,10 @@
 // itself.  All arithmetic is fp32, rounded once on the way out.
 //
 // Measured, 16384 tokens of 16 query, 16 key and 16 value heads of 128: forward
-// 69 us for 407 MB (90 % of the measured copy bandwidth; 87 us with the rows in
-// flight held in registers), backward 103 us for 541 MB (80 %; 191 us so).  The
-// forward's rest is the last wave; the backward issues in 70 % of its cycles
-// with the four warps a scheduler has room for.
+// 67 to 70 us for 407 MB (89 to 93 % of the measured copy bandwidth; 87 us with
+// the rows in flight held in registers), backward 99 us for 541 MB (84 %; 191 us
+// so).  The same reads and writes without the arithmetic take the backward 93 us.
+// Packed fp32 pairs and a loader without branches took 4 and 9 % off.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -77,18 +77,30 @@ struct PrepOut {
 
 constexpr int kRopeThreads = 256;
 
-__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
+// The eight bf16 of a lane's 16 bytes as four pairs of fp32 (for packed
+// arithmetic), and back.
+__device__ __forceinline__ void widen8(const uint4& w, uint64_t (&x)[4]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+        x[i] = f2_pack(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow8(const uint64_t (&x)[4]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_unpack(x[i], lo, hi);
+        u[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ float sum_pair(uint64_t x) {
+    float lo, hi;
+    f2_unpack(x, lo, hi);
+    return lo + hi;
 }
 
 __device__ __forceinline__ float weight_at(const void* w, int f32, int i) {
@@ -104,73 +116,87 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+// The same of two numbers: lanes of one parity add the first, the others the
+// second, and the parities exchange them (five shuffles instead of eight).
+template <int LANES>
+__device__ __forceinline__ void row_sum2(float& a, float& b, int lane) {
+    const bool odd = lane & 1;
+    float keep = odd ? b : a;
+    keep += __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+#pragma unroll
+    for (int o = 2; o < LANES; o <<= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+    const float other = __shfl_xor_sync(0xffffffffu, keep, 1);
+    a = odd ? other : keep;
+    b = odd ? keep : other;
+}
+
 // One lane's share of the rotation: it holds values [8c, 8c + 8) of a row.
+// Values beyond rope_dim take cosine 1, sine 0 and a partner of 0.
 template <int D, bool INTERLEAVED>
 struct Turn {
     static constexpr int LANES = D / 8;
-    bool on;        // these values are turned
     int src;        // lane that holds the other members of the pairs
     int other;      // index of the pair partner of value 8c (INTERLEAVED: unused)
-    float sign;     // -1: this lane holds the pairs' first members
-    float c[8], s[8];
+    uint32_t seen;  // mask of the partners' bits
+    uint64_t c[4];  // cosines, and sines with the sign that a value's partner takes
+    uint64_t s[4];  // in the turn (minus for a pair's first member)
 
     // c and s of every value, from the token's row of the table.
     __device__ __forceinline__ void load(const RopeParams& p, long long pos, int lane) {
         const int col = lane & (LANES - 1), e0 = 8 * col;
-        on = e0 < p.rope_dim;
         src = lane;
         other = e0;
-        sign = -1.f;
-        if (!on) return;
+        seen = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = f2_pack(1.f, 1.f);
+            s[i] = 0ull;
+        }
+        if (e0 >= p.rope_dim) return;
+        seen = 0xffffffffu;
         const float4* row =
             reinterpret_cast<const float4*>(p.table + pos * (p.rope_dim / 2));
         if constexpr (INTERLEAVED) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // two pairs per 16 bytes
                 const float4 f = __ldg(row + 2 * col + i);
-                c[4 * i] = c[4 * i + 1] = f.x;
-                s[4 * i] = s[4 * i + 1] = f.y;
-                c[4 * i + 2] = c[4 * i + 3] = f.z;
-                s[4 * i + 2] = s[4 * i + 3] = f.w;
+                c[2 * i] = f2_pack(f.x, f.x);
+                s[2 * i] = f2_pack(-f.y, f.y);
+                c[2 * i + 1] = f2_pack(f.z, f.z);
+                s[2 * i + 1] = f2_pack(-f.w, f.w);
             }
         } else {
             const int half = p.rope_dim / 2;
             const bool second = e0 >= half;
-            sign = second ? 1.f : -1.f;
+            const float sign = second ? 1.f : -1.f;
             other = second ? e0 - half : e0 + half;
             src = (lane & ~(LANES - 1)) | (other >> 3);
             const int i0 = second ? e0 - half : e0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 f = __ldg(row + i0 / 2 + i);
-                c[2 * i] = f.x;
-                s[2 * i] = f.y;
-                c[2 * i + 1] = f.z;
-                s[2 * i + 1] = f.w;
+                c[i] = f2_pack(f.x, f.z);
+                s[i] = f2_pack(sign * f.y, sign * f.w);
             }
         }
     }
 
-    __device__ __forceinline__ float sign_of(int j) const {
-        return INTERLEAVED ? ((j & 1) ? 1.f : -1.f) : sign;
-    }
     __device__ __forceinline__ int partner_index(int e0, int j) const {
         return INTERLEAVED ? (e0 + (j ^ 1)) : (other + j);
     }
     // The pair partners of the eight values in `w` (all lanes take part).
-    __device__ __forceinline__ void partners(const uint4& w, const float (&x)[8],
-                                             float (&y)[8]) const {
+    __device__ __forceinline__ void partners(const uint4& w, uint64_t (&y)[4]) const {
+        uint4 t;
         if constexpr (INTERLEAVED) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+            t = make_uint4(__byte_perm(w.x, 0, 0x1032), __byte_perm(w.y, 0, 0x1032),
+                           __byte_perm(w.z, 0, 0x1032), __byte_perm(w.w, 0, 0x1032));
         } else {
-            uint4 t;
             t.x = __shfl_sync(0xffffffffu, w.x, src);
             t.y = __shfl_sync(0xffffffffu, w.y, src);
             t.z = __shfl_sync(0xffffffffu, w.z, src);
             t.w = __shfl_sync(0xffffffffu, w.w, src);
-            widen8(t, y);
         }
+        widen8(make_uint4(t.x & seen, t.y & seen, t.z & seen, t.w & seen), y);
     }
 };
 
@@ -359,17 +385,18 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
         // y_j = rstd * (x_j * own_j + partner_j * cross_j)
         Turn<D, INTERLEAVED> turn;
         turn.load(p, pos, lane);
-        float own[8], cross[8];
+        uint64_t own[4], cross[4];
         const void* wt = part == 0 ? p.wq : p.wk;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float w0 = norm ? weight_at(wt, p.w_f32, e0 + j) : 1.f;
-            own[j] = turn.on ? w0 * turn.c[j] : w0;
-            cross[j] = 0.f;
-            if (turn.on) {
-                const float w1 =
-                    norm ? weight_at(wt, p.w_f32, turn.partner_index(e0, j)) : 1.f;
-                cross[j] = turn.sign_of(j) * w1 * turn.s[j];
+        for (int i = 0; i < 4; ++i) {
+            own[i] = turn.c[i];
+            cross[i] = turn.s[i];
+            if (norm) {
+                const int o = turn.partner_index(e0, 2 * i), o1 = turn.partner_index(e0, 2 * i + 1);
+                own[i] = fmul2(own[i], f2_pack(weight_at(wt, p.w_f32, e0 + 2 * i),
+                                               weight_at(wt, p.w_f32, e0 + 2 * i + 1)));
+                cross[i] = fmul2(cross[i], f2_pack(weight_at(wt, p.w_f32, o),
+                                                   weight_at(wt, p.w_f32, o1)));
             }
         }
 #pragma unroll 1
@@ -382,19 +409,20 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
             load();
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                float x[8], xp[8], y[8];
+                uint64_t x[4], xp[4], y[4];
                 widen8(w[u], x);
-                turn.partners(w[u], x, xp);
+                turn.partners(w[u], xp);
                 float rstd = 1.f;
                 if (norm) {
-                    float ss = 0.f;
+                    uint64_t ss = fmul2(x[0], x[0]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-                    rstd = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + p.eps);
+                    for (int i = 1; i < 4; ++i) ss = ffma2(x[i], x[i], ss);
+                    rstd = rsqrtf(row_sum<LANES>(sum_pair(ss)) * (1.f / D) + p.eps);
                 }
+                const uint64_t rstd2 = f2_pack(rstd, rstd);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[j] = rstd * (turn.on ? fmaf(x[j], own[j], xp[j] * cross[j]) : x[j] * own[j]);
+                for (int i = 0; i < 4; ++i)
+                    y[i] = fmul2(rstd2, ffma2(xp[i], cross[i], fmul2(x[i], own[i])));
                 if (h + u < r.z && write) *reinterpret_cast<uint4*>(to + u * step) = narrow8(y);
             }
             to += 2 * step;
@@ -407,26 +435,26 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
 // few whole blocks and two parts of one.  With a norm it leaves its sums of dw
 // for queries and keys in `part` [CTAs][2][D], which fa_dw_reduce_kernel adds
 // up in a fixed order.
-template <int D, bool INTERLEAVED>
+template <int D, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, 2)
     fa_prep_bwd_kernel(const HeadRows dyq, const HeadRows dyk, const HeadRows dyv,
                        const HeadRows xq, const HeadRows xk, const HeadRowsOut dq,
                        const HeadRowsOut dk, const HeadRowsOut dv, const RopeParams p,
                        long long per_cta, float* part_dw) {
-    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, SLOTS = 5;
-    __shared__ __align__(16) uint8_t ring_mem[RowRing<SLOTS>::BYTES];
-    const RowRing<SLOTS> ring{smem_u32(ring_mem) + threadIdx.x * 16u};
+    constexpr int LANES = D / 8, TOKENS = kRopeThreads / LANES, SLOTS = 6;
+    using Ring = RowRing<SLOTS>;
+    __shared__ __align__(16) uint8_t ring_mem[Ring::BYTES];
+    const Ring ring{smem_u32(ring_mem) + threadIdx.x * 16u};
     const int lane = threadIdx.x & 31;
     const int col = threadIdx.x & (LANES - 1), e0 = 8 * col;
     const long long total = static_cast<long long>(p.B) * p.N;
     const int heads = p.Hq + p.Hkv + (dyv.p ? p.Hkv : 0);
-    const bool norm = p.wq != nullptr;
     const long long first_head = blockIdx.x * per_cta;
     const long long last_head =
         min(first_head + per_cta, (total + TOKENS - 1) / TOKENS * heads);
-    float dw[2][8];
+    uint64_t dw[2][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
+    for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = 0ull;
 
     // An item: the token (b, n) and its heads [h0, h1).
     struct Item {
@@ -447,12 +475,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
         return x;
     };
     // The loader runs SLOTS - 1 steps ahead, over the borders of items.  A
-    // step is a head's gradient and (with a norm) row, or two value heads.
+    // step is a head's gradient and (NORM) row, or two value heads (one, twice,
+    // where their number is odd).
     long long load_at = first_head;
-    int load_part = -1, load_left = 0, load_slot = 0;
-    const __nv_bfloat16 *load_g = nullptr, *load_x = nullptr;
-    long long load_gs = 0, load_xs = 0;
-    auto load = [&]() {
+    int load_part = -1, load_left = 0;
+    const __nv_bfloat16 *load_a = nullptr, *load_b = nullptr;
+    long long step_a = 0, step_b = 0;
+    auto seek = [&]() {
         while (load_left == 0 && load_at < last_head) {
             const Item x = item_at(load_at);
             if (++load_part == 3) {
@@ -463,35 +492,47 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
             const PartRange r(p, load_part, x.h0, x.h1);
             if (r.a >= r.z) continue;
             const HeadRows& dy = load_part == 0 ? dyq : load_part == 1 ? dyk : dyv;
-            const HeadRows& in = load_part == 0 ? xq : xk;
             load_left = r.z - r.a;
-            load_g = dy.p + x.b * dy.sb + x.n * dy.sn + (r.a - r.first) * dy.sh + e0;
-            load_gs = dy.sh;
-            if (norm) {
-                load_x = in.p + x.b * in.sb + x.n * in.sn + (r.a - r.first) * in.sh + e0;
-                load_xs = in.sh;
+            load_a = dy.p + x.b * dy.sb + x.n * dy.sn + (r.a - r.first) * dy.sh + e0;
+            load_b = load_a;
+            step_a = step_b = dy.sh;
+            if (load_part == 2) {
+                if (load_left % 2 == 0) {
+                    load_b = load_a + dy.sh;
+                    step_a = step_b = 2 * dy.sh;
+                    load_left /= 2;
+                }
+            } else if (NORM) {
+                const HeadRows& in = load_part == 0 ? xq : xk;
+                load_b = in.p + x.b * in.sb + x.n * in.sn + (r.a - r.first) * in.sh + e0;
+                step_b = in.sh;
             }
         }
+    };
+    auto load = [&](int slot) {
         if (load_left > 0) {
-            ring.put(load_slot, 0, load_g);
-            if (load_part == 2) {
-                if (load_left > 1) ring.put(load_slot, 1, load_g + load_gs);
-                load_g += 2 * load_gs;
-                load_left = max(0, load_left - 2);
-            } else {
-                if (norm) ring.put(load_slot, 1, load_x);
-                load_g += load_gs;
-                load_x += load_xs;
-                --load_left;
-            }
-            load_slot = ring.next(load_slot);
+            ring.put(slot, 0, load_a);
+            if (NORM || load_part == 2) ring.put(slot, 1, load_b);
+            load_a += step_a;
+            load_b += step_b;
+            if (--load_left == 0) seek();
         }
         ring.commit();
     };
+    seek();
 #pragma unroll
-    for (int i = 0; i < SLOTS - 1; ++i) load();
+    for (int i = 0; i < SLOTS - 1; ++i) load(i);
 
-    int slot = 0;
+    // The slot that the last step read is free again.
+    int slot = 0, freed = SLOTS - 1;
+    auto take = [&](uint4& a, uint4& b) {
+        ring.wait();
+        a = ring.get(slot, 0);
+        b = ring.get(slot, 1);
+        load(freed);
+        freed = slot;
+        slot = ring.next(slot);
+    };
 #pragma unroll 1
     for (long long at = first_head; at < last_head;) {
         const Item x = item_at(at);
@@ -506,59 +547,54 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
             const HeadRowsOut& dx = part == 0 ? dq : part == 1 ? dk : dv;
             __nv_bfloat16* to = dx.p + x.b * dx.sb + x.n * dx.sn + (r.a - r.first) * dx.sh + e0;
             if (part == 2) {
+                const bool two = (r.z - r.a) % 2 == 0;
 #pragma unroll 1
-                for (int h = r.a; h < r.z; h += 2) {
-                    ring.wait();
-                    const uint4 w0 = ring.get(slot, 0), w1 = ring.get(slot, 1);
-                    slot = ring.next(slot);
-                    load();
+                for (int h = r.a; h < r.z; h += two ? 2 : 1) {
+                    uint4 w0, w1;
+                    take(w0, w1);
                     if (x.active) *reinterpret_cast<uint4*>(to) = w0;
-                    if (x.active && h + 1 < r.z) *reinterpret_cast<uint4*>(to + dx.sh) = w1;
-                    to += 2 * dx.sh;
+                    if (x.active && two) *reinterpret_cast<uint4*>(to + dx.sh) = w1;
+                    to += two ? 2 * dx.sh : dx.sh;
                 }
                 continue;
             }
-            float w[8];
+            uint64_t w[4];
+            if constexpr (NORM) {
+                const void* wt = part == 0 ? p.wq : p.wk;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                w[j] = norm ? weight_at(part == 0 ? p.wq : p.wk, p.w_f32, e0 + j) : 1.f;
+                for (int i = 0; i < 4; ++i)
+                    w[i] = f2_pack(weight_at(wt, p.w_f32, e0 + 2 * i),
+                                   weight_at(wt, p.w_f32, e0 + 2 * i + 1));
+            }
 #pragma unroll 1
             for (int h = r.a; h < r.z; ++h) {
-                ring.wait();
-                const uint4 gr = ring.get(slot, 0);
-                uint4 xr = make_uint4(0u, 0u, 0u, 0u);
-                if (norm) xr = ring.get(slot, 1);
-                slot = ring.next(slot);
-                load();
-                float g[8], gp[8], y[8];
+                uint4 gr, xr;
+                take(gr, xr);
+                uint64_t g[4], gp[4], y[4];
                 widen8(gr, g);
-                turn.partners(gr, g, gp);
-                if (turn.on) {
+                turn.partners(gr, gp);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)  // the turn's transpose
-                        y[j] = fmaf(g[j], turn.c[j], -turn.sign_of(j) * gp[j] * turn.s[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = g[j];
-                }
-                if (norm) {
-                    float v[8];
+                for (int i = 0; i < 4; ++i)  // the turn's transpose: g c - gp s
+                    y[i] = fsub2(fmul2(g[i], turn.c[i]), fmul2(gp[i], turn.s[i]));
+                if constexpr (NORM) {
+                    uint64_t v[4], t[4], ss2, gx2;
                     widen8(xr, v);
-                    float ss = 0.f, gx = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        ss += v[j] * v[j];
-                        gx += y[j] * w[j] * v[j];
+                    for (int i = 0; i < 4; ++i) {
+                        t[i] = fmul2(y[i], w[i]);
+                        ss2 = i ? ffma2(v[i], v[i], ss2) : fmul2(v[i], v[i]);
+                        gx2 = i ? ffma2(t[i], v[i], gx2) : fmul2(t[i], v[i]);
                     }
-                    ss = row_sum<LANES>(ss);
-                    gx = row_sum<LANES>(gx);
+                    float ss = sum_pair(ss2), gx = sum_pair(gx2);
+                    row_sum2<LANES>(ss, gx, lane);
                     const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
-                    const float along = gx * rstd * (1.f / D);
+                    const float along = gx * rstd * (-1.f / D) * rstd;
+                    const uint64_t rstd2 = f2_pack(rstd, rstd), along2 = f2_pack(along, along);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float xh = v[j] * rstd;
-                        if (x.active) dw[part == 0 ? 0 : 1][j] += y[j] * xh;
-                        y[j] = rstd * (y[j] * w[j] - xh * along);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t xh = fmul2(v[i], rstd2);
+                        if (x.active) dw[part][i] = ffma2(y[i], xh, dw[part][i]);
+                        y[i] = ffma2(xh, along2, fmul2(t[i], rstd2));
                     }
                 }
                 if (x.active) *reinterpret_cast<uint4*>(to) = narrow8(y);
@@ -566,16 +602,19 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
             }
         }
     }
-    if (!norm) return;
+    if constexpr (!NORM) return;
 
     // The CTA's sums: over the rows of each warp by shuffles, then over the
-    // warps through shared memory.
-    __shared__ float red[kRopeThreads / 32][2][D];
+    // warps through shared memory (the ring's: its copies have all been read).
+    auto red = reinterpret_cast<float(*)[2][D]>(ring_mem);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float x = dw[i][j];
+            float lo, hi;
+            f2_unpack(dw[i][j / 2], lo, hi);
+            float x = j & 1 ? hi : lo;
 #pragma unroll
             for (int o = LANES; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             if (lane < LANES) red[threadIdx.x >> 5][i][e0 + j] = x;
@@ -589,25 +628,28 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     }
 }
 
-// dw[c] = sum over `ctas` of part[cta][c]: 32 columns per CTA, 32 rows of
+// dw[c] = sum over `ctas` of part[cta][c]: 8 columns per CTA, 128 rows of
 // threads, always in the same order.
 template <int D>
 __global__ void __launch_bounds__(1024)
     fa_dw_reduce_kernel(const float* part, int ctas, float* dwq, float* dwk) {
-    __shared__ float red[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x;
+    __shared__ float red[32][9];
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+    const int c = blockIdx.x * 8 + x;
     grid_dependency_wait();
     float s = 0.f;
-#pragma unroll 8
-    for (int r = y; r < ctas; r += 32) s += part[static_cast<long long>(r) * 2 * D + c];
-    red[y][x] = s;
+#pragma unroll 5
+    for (int r = y; r < ctas; r += 128) s += part[static_cast<long long>(r) * 2 * D + c];
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][x] = s;
     __syncthreads();
-    s = red[x][y];
+    if (threadIdx.x >= 256) return;
+    s = red[threadIdx.x & 31][threadIdx.x >> 5];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (x == 0) {
-        const int col = blockIdx.x * 32 + y;
+    if ((threadIdx.x & 31) == 0) {
+        const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
         (col < D ? dwq : dwk)[col % D] = s;
     }
 }

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
         };
         bool ok = true;
         int issued = 0;
+        const uint64_t policy = l2_policy(p.row_tiles == 1);
         for (int j = 0; j < nblk && ok; ++j) {
             const bool mine = wants(j);
             const int z = mine ? page_plane(p, page, head) : 0;
@@ -235,9 +236,9 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
                         bar, static_cast<uint32_t>(boxes) * box * T::CHUNKS * 128u);
                 __syncwarp();
                 if (mine)
-                    tma_load_3d(smem + T::KV_OFF + slot * T::TILE_BYTES + c * T::CHUNK_BYTES +
-                                    (b << p.box_shift) * 128,
-                                h ? &tmV : &tmK, bar, c * 64, y, z);
+                    tma_load_3d_hint(smem + T::KV_OFF + slot * T::TILE_BYTES +
+                                         c * T::CHUNK_BYTES + (b << p.box_shift) * 128,
+                                     h ? &tmV : &tmK, bar, c * 64, y, z, policy);
                 ++issued;
             }
         }
@@ -825,6 +826,9 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
                                              : p.block_table +
                                                    static_cast<long long>(walk.s) * p.max_pages;
             int page = wants(0) ? table[key_of(0) >> p.page_shift] : 0;
+            // Keys of one row tile are read once: they leave L2 before the
+            // partial results that the merge will read.
+            const uint64_t policy = l2_policy(walk.seq.tiles == 1);
             for (int j = 0; j < nblk && ok; ++j) {
                 const int slot = issued % T::NSTAGE;
                 const bool mine = wants(j);
@@ -840,9 +844,9 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
                                           static_cast<uint32_t>(boxes) * box * T::CHUNKS * 256u);
                 __syncwarp();
                 if (mine)
-                    tma_load_3d(smem + slot * T::STAGE_BYTES + h * T::TILE_BYTES +
-                                    c * T::CHUNK_BYTES + (b << p.box_shift) * 128,
-                                h ? &tmV : &tmK, &full[slot], c * 64, y, z);
+                    tma_load_3d_hint(smem + slot * T::STAGE_BYTES + h * T::TILE_BYTES +
+                                         c * T::CHUNK_BYTES + (b << p.box_shift) * 128,
+                                     h ? &tmV : &tmK, &full[slot], c * 64, y, z, policy);
                 ++issued;
             }
         } while (ok && walk.next(p));

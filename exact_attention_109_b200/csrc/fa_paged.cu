@@ -155,44 +155,30 @@ bool prepare(int dev) {
     return g_ready[dev].ok;
 }
 
-template <class... Params, class... Args>
-cudaError_t launch(void (*kernel)(Params...), long long grid, int threads, size_t smem,
-                   bool overlap, cudaStream_t s, Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 template <int D>
 cudaError_t launch_all(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv,
                        const CUtensorMap& mp, const fa::PagedParams& prm, cudaStream_t s) {
+    using fa_host::launch_overlapped;
     cudaError_t e = cudaSuccess;
-    const bool prefix = pl.prefix_splits > 0;
-    if (prefix) {
-        const long long grid =
-            static_cast<long long>(prm.Hkv) * pl.row_tiles * pl.prefix_splits;
+    if (pl.prefix_splits > 0) {
+        const dim3 grid(prm.Hkv * pl.row_tiles * pl.prefix_splits);
         e = pl.tiles == 2
-                ? launch(fa::fa_prefix_kernel<D, 2>, grid, fa::PrefixTraits<D, 2>::NUM_THREADS,
-                         fa::PrefixTraits<D, 2>::SMEM_BYTES, false, s, mk, mv, mp, prm)
-                : launch(fa::fa_prefix_kernel<D, 1>, grid, fa::PrefixTraits<D, 1>::NUM_THREADS,
-                         fa::PrefixTraits<D, 1>::SMEM_BYTES, false, s, mk, mv, mp, prm);
+                ? launch_overlapped(fa::fa_prefix_kernel<D, 2>, grid,
+                                    fa::PrefixTraits<D, 2>::NUM_THREADS,
+                                    fa::PrefixTraits<D, 2>::SMEM_BYTES, s, mk, mv, mp, prm)
+                : launch_overlapped(fa::fa_prefix_kernel<D, 1>, grid,
+                                    fa::PrefixTraits<D, 1>::NUM_THREADS,
+                                    fa::PrefixTraits<D, 1>::SMEM_BYTES, s, mk, mv, mp, prm);
         if (e != cudaSuccess) return e;
     }
-    e = launch(fa::fa_own_kernel<D>, pl.line_ctas, fa::OwnTraits<D>::THREADS,
-               fa::OwnTraits<D>::SMEM_BYTES, prefix, s, mk, mv, prm);
+    e = launch_overlapped(fa::fa_own_kernel<D>, dim3(pl.line_ctas), fa::OwnTraits<D>::THREADS,
+                          fa::OwnTraits<D>::SMEM_BYTES, s, mk, mv, prm);
     if (e != cudaSuccess) return e;
-    const long long rows = static_cast<long long>(prm.T) * prm.Hq;
+    const int rows = prm.T * prm.Hq;
     return rows <= kWideMergeRows
-               ? launch(fa::fa_paged_merge_kernel<D, 4>, rows, 128, 0, true, s, prm)
-               : launch(fa::fa_paged_merge_kernel<D, 1>, (rows + 3) / 4, 128, 0, true, s, prm);
+               ? launch_overlapped(fa::fa_paged_merge_kernel<D, 4>, dim3(rows), 128, 0, s, prm)
+               : launch_overlapped(fa::fa_paged_merge_kernel<D, 1>, dim3((rows + 3) / 4), 128, 0, s,
+                                   prm);
 }
 
 }  // namespace

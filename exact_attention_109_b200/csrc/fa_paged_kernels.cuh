@@ -152,8 +152,6 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::MISC_OFF + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // The own-rows grid does not depend on this one and may start at once.
-    grid_launch_dependents();
     // Row tiles fastest: CTAs that read the same keys run together.
     int idx = blockIdx.x;
     const int rt = idx % p.row_tiles;
@@ -196,6 +194,10 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // What was enqueued before this call ends here; the own-rows grid does not
+    // depend on this one and may start then.
+    grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t tmem = *tmem_slot;
     const AbortState st{abort_flag, p.err};
     if (warp >= 4 * TILES) {
@@ -751,7 +753,7 @@ __device__ __forceinline__ void add_visible(const uint8_t* v, int r, int col,
 // Bound by HBM: with 4 * D bytes a key against 16 rows the mma.sync tiles need
 // less time than the reads (a 64-key stage of 128 takes 1.25 us of a CTA's
 // chain, its share of HBM 1.46 us with two CTAs an SM).  16 sequences of 8192
-// keys, 16 heads of 128: 169 to 184 us for 1.07 GB (89 to 97 % of the measured
+// keys, 16 heads of 128: 164 to 171 us for 1.07 GB (96 to 100 % of the measured
 // copy bandwidth).  Ragged short sequences pay the first 6 us, in which the
 // lengths, page table and first stages come in one after another, and 3.3 us a
 // tile beside its keys: 64 sequences of 512 keys on average, 8 heads of 128:
@@ -770,7 +772,6 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     volatile int* carry_on = abort_flag + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < T::NSTAGE; ++i) {
             mbar_init(&full[i], 1);
@@ -781,6 +782,10 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
+    // Behind a prefix this grid starts when the prefix's has seen the end of
+    // what came before; alone it waits for that itself.
+    if (!p.prefix_splits) grid_dependency_wait();
+    grid_launch_dependents();
     // Starts, lengths and counts out of range are reported once.
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.S; i += T::THREADS) {
@@ -797,8 +802,8 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
     // The merge waits for this grid only, so this grid ends after the prefix
     // grid (which it was allowed to overtake): its first CTA waits for that, at
     // its end, and keeps no other from its place.
-    auto leave = [] {
-        if (blockIdx.x == 0) grid_dependency_wait();
+    auto leave = [&] {
+        if (blockIdx.x == 0 && p.prefix_splits) grid_dependency_wait();
     };
     if (!any) {
         leave();
@@ -1149,8 +1154,8 @@ struct RowSum {
 
 // W warps per output row (token, query head): with w_x = 2^(lse_x - M) over
 // the row's partial results, O = sum_x w_x O_x / sum_x w_x.  What this costs is
-// its chain of dependent reads (7 us for 2048 rows of 17 results, 18 MB, behind
-// the last CTA of the line), so the prefix's first splits, whose places are
+// its chain of dependent reads (4 us for 2048 rows of 17 results, 18 MB, behind
+// the last CTA of the line; 7 while own keys pushed them out of L2), so the prefix's first splits, whose places are
 // known, are read at once with the row's table entry, and its first pieces
 // before any of them is added up.  Few rows may have many pieces (a long
 // sequence spread over the whole GPU): the row's warps take them in turn.
@@ -1162,6 +1167,7 @@ __global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParam
     const long long row = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
     const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - 1ll * t * p.Hq);
     const int head = hq / p.G, g = hq - head * p.G;
+    grid_launch_dependents();
     const bool mine = row < static_cast<long long>(p.T) * p.Hq && t >= p.seq_start[0] &&
                       t < p.seq_start[p.S];  // else no sequence's row
     const long long plane_row = static_cast<long long>(head) * p.R +

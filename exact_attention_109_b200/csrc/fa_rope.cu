@@ -113,8 +113,8 @@ cudaError_t launch_prep(const fa::HeadRows& q, const fa::HeadRows& k, const fa::
     const int groups = head_groups(blocks, heads);
     p.heads_per_cta = (heads + groups - 1) / groups;
     const dim3 grid(static_cast<unsigned>(blocks), (heads + p.heads_per_cta - 1) / p.heads_per_cta);
-    fa::fa_prep_kernel<D, IL, PAGED><<<grid, fa::kRopeThreads, 0, s>>>(q, k, v, p, out, dst);
-    return cudaGetLastError();
+    return fa_host::launch_overlapped(fa::fa_prep_kernel<D, IL, PAGED>, grid, fa::kRopeThreads, 0, s,
+                                      q, k, v, p, out, dst);
 }
 
 template <bool PAGED>
@@ -139,25 +139,14 @@ cudaError_t launch_prep_bwd(const fa::HeadRows (&dy)[3], const fa::HeadRows (&x)
     long long per_cta = std::max(kMinHeads, (units + kBwdCtas - 1) / kBwdCtas);
     if (per_cta >= 2 * kManyHeads) per_cta = (per_cta + 1) / 2;
     const int grid = static_cast<int>((units + per_cta - 1) / per_cta);
-    if (p.wq)
-        fa::fa_prep_bwd_kernel<D, IL, true><<<grid, fa::kRopeThreads, 0, s>>>(
-            dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2], p, per_cta, part);
-    else
-        fa::fa_prep_bwd_kernel<D, IL, false><<<grid, fa::kRopeThreads, 0, s>>>(
-            dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2], p, per_cta, part);
-    cudaError_t e = cudaGetLastError();
+    const auto kernel =
+        p.wq ? fa::fa_prep_bwd_kernel<D, IL, true> : fa::fa_prep_bwd_kernel<D, IL, false>;
+    const cudaError_t e = fa_host::launch_overlapped(kernel, dim3(grid), fa::kRopeThreads, 0, s, dy[0],
+                                                     dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2],
+                                                     p, per_cta, part);
     if (e != cudaSuccess || !p.wq) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * D / 8);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa::fa_dw_reduce_kernel<D>, static_cast<const float*>(part),
-                              grid, dwq, dwk);
+    return fa_host::launch_overlapped(fa::fa_dw_reduce_kernel<D>, dim3(2 * D / 8), 1024, 0, s,
+                                      static_cast<const float*>(part), grid, dwq, dwk);
 }
 
 fa::HeadRows rows_of(const void* p, const long long* s) {

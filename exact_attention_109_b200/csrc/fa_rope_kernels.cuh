@@ -20,9 +20,8 @@
 // itself.  All arithmetic is fp32, rounded once on the way out.
 //
 // Measured, 16384 tokens of 16 query, 16 key and 16 value heads of 128: forward
-// 67 to 70 us for 407 MB (89 to 93 % of the measured copy bandwidth; 87 us with
-// the rows in flight held in registers), backward 99 us for 541 MB (84 %; 191 us
-// so).  The same reads and writes without the arithmetic take the backward 93 us.
+// 67.5 us for 407 MB (92 % of the measured copy bandwidth; 87 us with the rows
+// in flight held in registers), backward 97 us for 541 MB (85 %; 191 us so).  The same reads and writes without the arithmetic take the backward 93 us.
 // Packed fp32 pairs and a loader without branches took 4 and 9 % off.
 #pragma once
 
@@ -312,6 +311,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
         }
         ring.commit();
     };
+    grid_dependency_wait();
+    grid_launch_dependents();
 #pragma unroll
     for (int i = 0; i < SLOTS - 1; ++i) load();
 
@@ -519,6 +520,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
         }
         ring.commit();
     };
+    grid_dependency_wait();
+    grid_launch_dependents();
     seek();
 #pragma unroll
     for (int i = 0; i < SLOTS - 1; ++i) load(i);

@@ -420,3 +420,91 @@ def test_two_graphs_share_a_workspace():
         torch.cuda.synchronize()
         for c, (o, l) in zip(cs, outs):
             ref.check(dict(c, lens=lens), o, l)
+
+
+@gpu
+@pytest.mark.parametrize("before", ["memset", "copy", "kernel", "other_stream", "nothing"])
+def test_order_behind_other_work(before):
+    """The calls start while the stream's previous work ends; what that wrote is
+    seen all the same, eagerly and in a captured graph, whatever kind it is."""
+    c = ref.make([1, 2], [40, 700], 300, 8, 4, 64, 16, seed=30)
+    want = run(c)
+    g = {n: (t.cuda() if isinstance(t, torch.Tensor) else t) for n, t in c.items()}
+    q, lens = torch.zeros_like(g["q"]), torch.zeros_like(g["len"])
+    big = torch.zeros(64 << 20, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        if before == "nothing":
+            q.copy_(g["q"])
+        elif before == "memset":
+            big.zero_()
+            q.copy_(g["q"])
+            lens.zero_()
+            lens.add_(g["len"])
+            big.zero_()
+        elif before == "copy":
+            lens.copy_(g["len"])
+            big.add_(1)
+            q.copy_(g["q"])
+        elif before == "kernel":
+            big.add_(1)
+            torch.add(g["len"], 0, out=lens)
+            torch.mul(g["q"], 1, out=q)
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                big.add_(1)
+                q.copy_(g["q"])
+                lens.copy_(g["len"])
+            torch.cuda.current_stream().wait_stream(side)
+        n = g["len"] if before == "nothing" else lens
+        return fa.attention_paged(q, g["k"], g["v"], g["table"], g["start"], n, c["scale"],
+                                  prefix_pages=g["prefix"], prefix_len=c["P"], max_new=2)
+
+    def reset():
+        q.fill_(NAN), lens.fill_(1)
+        torch.cuda.synchronize()
+
+    for _ in range(3):
+        reset()
+        got = step()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+def test_steps_in_a_row_keep_their_order():
+    """Twenty decoding steps without a host wait, each reading what the one
+    before appended, against the same steps one at a time."""
+    torch.manual_seed(5)
+    S, Hq, Hkv, d, page = 3, 8, 2, 128, 16
+    x = torch.randn(20, S, Hq + 2 * Hkv, d, device="cuda").bfloat16()
+    rope = fa.rope_table(64, d)
+    w = [torch.ones(d, device="cuda") for _ in range(2)]
+    table = torch.randperm(S * 4, device="cuda").int().view(S, 4)
+    start = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+
+    def steps(wait):
+        kp = torch.zeros(S * 4, Hkv, page, d, dtype=torch.bfloat16, device="cuda")
+        vp, have, outs = torch.zeros_like(kp), torch.tensor([0, 5, 17]).int().cuda(), []
+        for i in range(20):
+            o, have = _step(fa, x[i], kp, vp, table, start, have, rope, w, None, 0, (Hq, Hkv),
+                            d ** -0.5)
+            outs.append(o)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return torch.stack(outs), kp, vp
+
+    want = steps(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
+    assert fa.fa_get_device_error() == fa.FA_OK

@@ -508,3 +508,35 @@ def test_steps_in_a_row_keep_their_order():
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
     assert fa.fa_get_device_error() == fa.FA_OK
+
+
+@gpu
+@pytest.mark.parametrize("P", [0, 70])
+def test_many_sequences(P):
+    """More sequences than threads, some without tokens, in a table without spare columns."""
+    gen = torch.Generator().manual_seed(31)
+    new = torch.randint(0, 3, (1300,), generator=gen).tolist()
+    lens = [max(n, int(x)) for n, x in zip(new, torch.randint(0, 97, (1300,), generator=gen))]
+    c = ref.make(new, lens, P, 2, 1, 64, 32, seed=31)
+    c["table"] = c["table"][:, :-2].contiguous()
+    check(c)
+
+
+@gpu
+@pytest.mark.parametrize("Hkv,n,d", [(1, 30000, 64), (2, 9000, 128)])
+def test_one_sequence_over_the_whole_gpu(Hkv, n, d):
+    """A row tile whose keys all CTAs share: hundreds of partial results a row."""
+    check(ref.make([2], [n], 0, 4 * Hkv, Hkv, d, 128, seed=32))
+
+
+@gpu
+def test_more_row_tiles_than_splits():
+    """A prefix whose query rows alone fill the GPU."""
+    check(ref.make([300, 280, 310, 290], [300, 500, 310, 290], 400, 16, 2, 64, 64, seed=33))
+
+
+@gpu
+def test_rows_of_two_row_tiles_see_their_own_keys():
+    """Prompt chunks of many rows, whose tiles begin and end inside a token."""
+    check(ref.make([33, 7, 50], [200, 7, 129], 0, 10, 2, 128, 16, seed=34))
+    check(ref.make([33, 7, 50], [200, 7, 129], 130, 6, 2, 64, 256, seed=35))

@@ -410,7 +410,8 @@ PyObject* set_status_error(PyObject*, PyObject* type) {
     Py_RETURN_NONE;
 }
 
-#define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+#define FAST(f) \
+    {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(qk_norm_rope), FAST(qk_norm_rope_backward), FAST(paged_append),
                            FAST(attention_paged),
                            {"set_status_error", set_status_error, METH_O, nullptr},

@@ -25,6 +25,11 @@ constexpr int kMaxLineCtas = 444;
 // 16.7 / 20.1 / 71.5 against 21.0 / 24.5 / 69.7.  32 rows: 44.9 in the line
 // against 39.8 (16384 keys of 128).
 constexpr int kLinePrefixRows = 16;
+// Query rows of a key head up to which the prefix kernel takes them twice, with
+// heads of 64: 20 rows of 32 heads behind 4096 / 16384 / 65536 keys 31.6 / 50.7 /
+// 123 us, 32.7 / 56.4 / 143 with two idle softmax warps.  Heads of 128 are bound
+// by HBM there (199 us either way) and keep their rows once.
+constexpr int kHalvesRows = 64;
 // Output rows up to which the merge takes four warps for each: few rows may have
 // many pieces, many rows fill the GPU anyway.  32 rows behind 16384 keys: 22 us
 // with four, 34 with one; 16 rows behind 1024: 12.3 and 14.2; 2048 rows with 17
@@ -36,6 +41,7 @@ struct Plan {
     int row_tiles;        // prefix CTAs along the rows
     int prefix_splits, prefix_chunk;
     bool prefix_in_line;
+    bool halves;          // the two halves of every key block apart
     int slots;            // partial results of all rows
     int line_ctas;
 };
@@ -62,17 +68,23 @@ fa_status check_sizes(int S, int T, int Hq, int Hkv, int d, int page_size, int m
 
 // The prefix's tiles of query rows, and the splits that the workspace has room
 // for.
-Plan plan_rows(int T, int G, int Hkv, int prefix_len) {
+Plan plan_rows(int T, int G, int Hkv, int d, int prefix_len) {
     Plan pl{};
     const long long rows = static_cast<long long>(T) * G;
     pl.prefix_in_line = prefix_len > 0 && rows <= kLinePrefixRows;
     pl.tiles = rows > 128 ? 2 : 1;
+    pl.halves = d == 64 && rows <= kHalvesRows;
     pl.row_tiles = static_cast<int>((rows + 128 * pl.tiles - 1) / (128 * pl.tiles));
     const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
     if (prefix_len > 0 && !pl.prefix_in_line)
         pl.prefix_splits = static_cast<int>(std::min<long long>(
             (prefix_len + 127) / 128, std::max(1ll, kMaxPrefixCtas / units)));
     return pl;
+}
+
+// Partial results of the prefix for each row.
+int prefix_slots(const Plan& pl) {
+    return pl.prefix_in_line ? 1 : pl.prefix_splits * (pl.halves ? 2 : 1);
 }
 
 // CTAs of the line: as many as are resident, unless the longest line has less
@@ -91,7 +103,7 @@ int line_ctas(const Plan& pl, int S, int G, int Hkv, int d, int page_size, int m
 
 Plan make_plan(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages, int prefix_len,
                int max_new, int sm_count) {
-    Plan pl = plan_rows(T, Hq / Hkv, Hkv, prefix_len);
+    Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len);
     pl.line_ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
                              sm_count);
     if (pl.prefix_splits > 0) {
@@ -113,7 +125,7 @@ Plan make_plan(int S, int T, int Hq, int Hkv, int d, int page_size, int max_page
         pl.prefix_splits = static_cast<int>((blocks + best_per - 1) / best_per);
         pl.prefix_chunk = static_cast<int>(best_per) * 128;
     }
-    pl.slots = prefix_len == 0 ? 0 : 1 + (pl.prefix_in_line ? 1 : pl.prefix_splits);
+    pl.slots = prefix_len == 0 ? 0 : 1 + prefix_slots(pl);
     return pl;
 }
 
@@ -124,14 +136,14 @@ size_t table_bytes(int T, int Hq) {
 
 // Opts the kernel into its shared memory and checks that the registers it is
 // launched with cover its setmaxnreg split.
-template <int D, int TILES>
+template <int D, int TILES, bool HALVES>
 bool prepare_prefix() {
     using T = fa::PrefixTraits<D, TILES>;
     cudaFuncAttributes attr{};
-    return cudaFuncSetAttribute(fa::fa_prefix_kernel<D, TILES>,
+    return cudaFuncSetAttribute(fa::fa_prefix_kernel<D, TILES, HALVES>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 T::SMEM_BYTES) == cudaSuccess &&
-           cudaFuncGetAttributes(&attr, fa::fa_prefix_kernel<D, TILES>) == cudaSuccess &&
+           cudaFuncGetAttributes(&attr, fa::fa_prefix_kernel<D, TILES, HALVES>) == cudaSuccess &&
            attr.numRegs * T::NUM_THREADS >= T::REG_BUDGET;
 }
 template <int D>
@@ -148,8 +160,9 @@ Ready g_ready[kMaxDevices];
 
 bool prepare(int dev) {
     std::call_once(g_ready[dev].once, [&] {
-        g_ready[dev].ok = prepare_prefix<64, 1>() && prepare_prefix<64, 2>() &&
-                          prepare_prefix<128, 1>() && prepare_prefix<128, 2>() &&
+        g_ready[dev].ok = prepare_prefix<64, 1, true>() && prepare_prefix<64, 1, false>() &&
+                          prepare_prefix<64, 2, false>() && prepare_prefix<128, 1, false>() &&
+                          prepare_prefix<128, 2, false>() &&
                           prepare_own<64>() && prepare_own<128>();
     });
     return g_ready[dev].ok;
@@ -162,13 +175,15 @@ cudaError_t launch_all(const Plan& pl, const CUtensorMap& mk, const CUtensorMap&
     cudaError_t e = cudaSuccess;
     if (pl.prefix_splits > 0) {
         const dim3 grid(prm.Hkv * pl.row_tiles * pl.prefix_splits);
-        e = pl.tiles == 2
-                ? launch_overlapped(fa::fa_prefix_kernel<D, 2>, grid,
-                                    fa::PrefixTraits<D, 2>::NUM_THREADS,
-                                    fa::PrefixTraits<D, 2>::SMEM_BYTES, s, mk, mv, mp, prm)
-                : launch_overlapped(fa::fa_prefix_kernel<D, 1>, grid,
-                                    fa::PrefixTraits<D, 1>::NUM_THREADS,
-                                    fa::PrefixTraits<D, 1>::SMEM_BYTES, s, mk, mv, mp, prm);
+        if (pl.tiles == 2)
+            e = launch_overlapped(fa::fa_prefix_kernel<D, 2, false>, grid,
+                                  fa::PrefixTraits<D, 2>::NUM_THREADS,
+                                  fa::PrefixTraits<D, 2>::SMEM_BYTES, s, mk, mv, mp, prm);
+        else
+            e = launch_overlapped(pl.halves ? fa::fa_prefix_kernel<D, 1, D == 64>
+                                            : fa::fa_prefix_kernel<D, 1, false>,
+                                  grid, fa::PrefixTraits<D, 1>::NUM_THREADS,
+                                  fa::PrefixTraits<D, 1>::SMEM_BYTES, s, mk, mv, mp, prm);
         if (e != cudaSuccess) return e;
     }
     e = launch_overlapped(fa::fa_own_kernel<D>, dim3(pl.line_ctas), fa::OwnTraits<D>::THREADS,
@@ -191,10 +206,10 @@ size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d, int page_si
         T == 0)
         return 0;
     // Enough for any SM count: the splits are bounded by the sizes alone.
-    const Plan pl = plan_rows(T, Hq / Hkv, Hkv, prefix_len);
+    const Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len);
     const int ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
                                kMaxLineCtas);
-    const size_t slots = prefix_len == 0 ? 0 : 1 + (pl.prefix_in_line ? 1 : pl.prefix_splits);
+    const size_t slots = prefix_len == 0 ? 0 : 1 + prefix_slots(pl);
     return table_bytes(T, Hq) + (slots * T * Hq + ctas * 2 * 16) * (d + 1) * sizeof(float);
 }
 
@@ -272,6 +287,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
     prm.prefix_len = prefix_len;
     prm.prefix_splits = pl.prefix_splits;
     prm.prefix_chunk = pl.prefix_chunk;
+    prm.prefix_slots = pl.prefix_splits > 0 ? pl.slots - 1 : 0;
     prm.row_tiles = pl.row_tiles;
     prm.prefix_in_line = pl.prefix_in_line;
     prm.slots = pl.slots;
@@ -287,7 +303,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
     mp = mk;  // unused without a prefix
     if (pl.prefix_splits > 0 &&
         !fa_host::encode_map(&mp, prm.part_o, 4, d, prm.R,
-                             static_cast<long long>(pl.prefix_splits) * Hkv, 32, 32))
+                             static_cast<long long>(prm.prefix_slots) * Hkv, 32, 32))
         return FA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = d == 64 ? launch_all<64>(pl, mk, mv, mp, prm, s)

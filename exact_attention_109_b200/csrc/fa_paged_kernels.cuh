@@ -60,6 +60,7 @@ struct PagedParams {
     int page_shift, box_shift;  // log2 of the page's and of a TMA box's rows
     int num_pages, max_pages, max_new;
     int prefix_len, prefix_splits, prefix_chunk, row_tiles;
+    int prefix_slots;         // partial results of the prefix: splits, or twice that (HALVES)
     int prefix_in_line;       // the prefix is one more sequence of the line
     int slots, line_ctas;
     float scale_log2;         // scale * log2(e)
@@ -128,14 +129,20 @@ struct PrefixTraits {
 // tile's chain of score product, softmax and value product; set-up 4 us, the
 // partial results 3 us.  1024 rows behind 65536 keys of 4 heads: 113 to 125 us.
 // One tile, heads of 64: 1.05 us a block, the softmax of the warps that have
-// rows.  Moving exponentials to the FMA pipes or handing P over in halves
+// rows, 0.9 with HALVES.  Moving exponentials to the FMA pipes or handing P over in halves
 // changed nothing or made it slower.
-template <int D, int TILES>
+//
+// HALVES: at most 64 query rows.  They stand in the tile twice, and the two
+// copies take a half of every block's keys each, so that all four softmax warps
+// have work and half as much of it; the copies' results are joined like those
+// of two splits.
+template <int D, int TILES, bool HALVES>
 __global__ void __launch_bounds__(128 * (TILES + 1), 1)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmP, const PagedParams p) {
     using T = PrefixTraits<D, TILES>;
+    static_assert(!HALVES || TILES == 1, "one tile holds both copies");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bar_q = reinterpret_cast<uint64_t*>(smem + T::BAR_OFF);
@@ -348,7 +355,9 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
         // ------------------------------------------------ softmax warpgroups
         if constexpr (TILES == 2) setmaxnreg_inc<T::REG_SOFTMAX>();
         const int t = warp >> 2, lg = warp & 3;
-        const int wrow0 = r0 + 128 * t + lg * 32;  // this warp's first query row
+        const int half = HALVES ? lg >> 1 : 0;
+        // This warp's first query row.
+        const int wrow0 = HALVES ? (lg & 1) * 32 : r0 + 128 * t + lg * 32;
         const int row = wrow0 + lane;
         // Query rows of the warp into the swizzled tile (rows past R: zeros),
         // all copies in flight at once: through registers, four at a time, this
@@ -385,20 +394,22 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
             if (!ok) break;
             tc_fence_after();
             if (live) {
-                uint32_t sr[4][32];
+                constexpr int NC = HALVES ? 64 : 128;  // this thread's keys of the block
+                uint32_t sr[NC / 32][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32u * c, sr[c]);
+                for (int c = 0; c < NC / 32; ++c)
+                    tmem_ld32(s_tm + 64u * half + 32u * c, sr[c]);
                 tmem_ld_wait();
                 if (tail && j == nblk - 1) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= tail) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+                    for (int c = 0; c < NC; ++c)
+                        if (c + 64 * half >= tail) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
                 }
                 float mx[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mx[i] = __uint_as_float(sr[0][i]);
 #pragma unroll
-                for (int c = 8; c < 128; c += 8)
+                for (int c = 8; c < NC; c += 8)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         mx[i] = fmaxf(mx[i], __uint_as_float(sr[(c + i) >> 5][(c + i) & 31]));
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
                 uint64_t sum2[2] = {0ull, 0ull};
                 float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < NC / 64; ++h) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -455,7 +466,13 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
                         pk[e] = pack_bf16x2(p0, p1);
                         add_bf16x2_to_f32(pk[e], rs[2 * (e & 1)], rs[2 * (e & 1) + 1]);
                     }
-                    tmem_st32(s_tm + 32u * h, pk);
+                    tmem_st32(s_tm + 32u * (h + half), pk);
+                }
+                if constexpr (HALVES) {  // the other copy's keys weigh nothing here
+                    uint32_t zero[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) zero[e] = 0u;
+                    tmem_st32(s_tm + 32u * (1 - half), zero);
                 }
                 float a0, a1;
                 f2_unpack(fadd2(sum2[0], sum2[1]), a0, a1);
@@ -471,7 +488,7 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
             tc_fence_after();
             const bool none = l == 0.f;  // (a NaN score leaves l a NaN)
             const float inv = none ? 0.f : 1.f / lr;
-            const int plane = split * p.Hkv + head;
+            const int plane = (HALVES ? 2 * split + half : split) * p.Hkv + head;
             // O (fp32) leaves 32 columns at a time through this warp's rows of
             // the query tile, which no MMA reads any more.
 #pragma unroll 1
@@ -1155,10 +1172,11 @@ struct RowSum {
 // W warps per output row (token, query head): with w_x = 2^(lse_x - M) over
 // the row's partial results, O = sum_x w_x O_x / sum_x w_x.  What this costs is
 // its chain of dependent reads (4 us for 2048 rows of 17 results, 18 MB, behind
-// the last CTA of the line; 7 while own keys pushed them out of L2), so the prefix's first splits, whose places are
-// known, are read at once with the row's table entry, and its first pieces
-// before any of them is added up.  Few rows may have many pieces (a long
-// sequence spread over the whole GPU): the row's warps take them in turn.
+// the last CTA of the line; 7 while own keys pushed them out of L2), so the
+// prefix's first splits, whose places are known, are read at once with the row's
+// table entry, and its first pieces before any of them is added up.  Few rows
+// may have many pieces (a long sequence spread over the whole GPU): the row's
+// warps take them in turn.
 template <int D, int W>
 __global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParams p) {
     constexpr int PER = D / 32, U = 8, V = 4;
@@ -1194,7 +1212,7 @@ __global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParam
     int2 pre = make_int2(0, 0);
     if (p.prefix_in_line) pre = pieces_of(1);
     auto load_splits = [&](int x0, float (&v)[U][PER]) {
-        const int n = min(U, p.prefix_splits - x0);
+        const int n = min(U, p.prefix_slots - x0);
         const long long r = plane_row + x0 * step;
         float ls = -INFINITY;
         if (lane < n) ls = p.part_lse[r + lane * step];
@@ -1228,9 +1246,9 @@ __global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParam
     float split_ls = load_splits(U * part, splits);
     if (p.prefix_len == 0 && own.x == 1) return;  // written by its CTA
     float piece_ls = load_pieces(V * part, pieces);
-    for (int x = U * part; x < p.prefix_splits;) {
+    for (int x = U * part; x < p.prefix_slots;) {
         sum.add(splits, split_ls);
-        if ((x += U * W) < p.prefix_splits) split_ls = load_splits(x, splits);
+        if ((x += U * W) < p.prefix_slots) split_ls = load_splits(x, splits);
     }
     for (int x = V * part; x < pre.x + own.x;) {
         sum.add(pieces, piece_ls);

@@ -113,8 +113,8 @@ cudaError_t launch_prep(const fa::HeadRows& q, const fa::HeadRows& k, const fa::
     const int groups = head_groups(blocks, heads);
     p.heads_per_cta = (heads + groups - 1) / groups;
     const dim3 grid(static_cast<unsigned>(blocks), (heads + p.heads_per_cta - 1) / p.heads_per_cta);
-    return fa_host::launch_overlapped(fa::fa_prep_kernel<D, IL, PAGED>, grid, fa::kRopeThreads, 0, s,
-                                      q, k, v, p, out, dst);
+    return fa_host::launch_overlapped(fa::fa_prep_kernel<D, IL, PAGED>, grid, fa::kRopeThreads, 0,
+                                      s, q, k, v, p, out, dst);
 }
 
 template <bool PAGED>
@@ -141,9 +141,9 @@ cudaError_t launch_prep_bwd(const fa::HeadRows (&dy)[3], const fa::HeadRows (&x)
     const int grid = static_cast<int>((units + per_cta - 1) / per_cta);
     const auto kernel =
         p.wq ? fa::fa_prep_bwd_kernel<D, IL, true> : fa::fa_prep_bwd_kernel<D, IL, false>;
-    const cudaError_t e = fa_host::launch_overlapped(kernel, dim3(grid), fa::kRopeThreads, 0, s, dy[0],
-                                                     dy[1], dy[2], x[0], x[1], dx[0], dx[1], dx[2],
-                                                     p, per_cta, part);
+    const cudaError_t e = fa_host::launch_overlapped(
+        kernel, dim3(grid), fa::kRopeThreads, 0, s, dy[0], dy[1], dy[2], x[0], x[1], dx[0], dx[1],
+        dx[2], p, per_cta, part);
     if (e != cudaSuccess || !p.wq) return e;
     return fa_host::launch_overlapped(fa::fa_dw_reduce_kernel<D>, dim3(2 * D / 8), 1024, 0, s,
                                       static_cast<const float*>(part), grid, dwq, dwk);

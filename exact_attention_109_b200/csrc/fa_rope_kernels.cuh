@@ -21,7 +21,8 @@
 //
 // Measured, 16384 tokens of 16 query, 16 key and 16 value heads of 128: forward
 // 67.5 us for 407 MB (92 % of the measured copy bandwidth; 87 us with the rows
-// in flight held in registers), backward 97 us for 541 MB (85 %; 191 us so).  The same reads and writes without the arithmetic take the backward 93 us.
+// in flight held in registers), backward 97 us for 541 MB (85 %; 191 us so).
+// The same reads and writes without the arithmetic take the backward 93 us.
 // Packed fp32 pairs and a loader without branches took 4 and 9 % off.
 #pragma once
 
@@ -254,7 +255,9 @@ struct RowRing {
                      : "memory");
         return v;
     }
-    static __device__ __forceinline__ int next(int slot) { return slot + 1 == SLOTS ? 0 : slot + 1; }
+    static __device__ __forceinline__ int next(int slot) {
+        return slot + 1 == SLOTS ? 0 : slot + 1;
+    }
 };
 
 // The heads [a, z) of part 0, 1, 2 (queries, keys, values) among [h0, h1).

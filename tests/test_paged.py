@@ -77,7 +77,8 @@ def test_split_plan_covers_the_keys_within_the_workspace(S, max_new, Hq, Hkv, P,
                 assert (splits == 0) == (P == 0 or in_line)
                 if splits:
                     assert chunk % 128 == 0 and (splits - 1) * chunk < P <= splits * chunk
-                slots = 0 if P == 0 else 1 + (1 if in_line else splits)
+                twice = 2 if d == 64 and T * Hq // Hkv <= 64 else 1
+                slots = 0 if P == 0 else 1 + (1 if in_line else twice * splits)
                 rows = slots * T * Hq + ctas * 2 * 16
                 assert 2 * T * Hq * 8 + rows * (d + 1) * 4 <= have
 
@@ -540,3 +541,15 @@ def test_rows_of_two_row_tiles_see_their_own_keys():
     """Prompt chunks of many rows, whose tiles begin and end inside a token."""
     check(ref.make([33, 7, 50], [200, 7, 129], 0, 10, 2, 128, 16, seed=34))
     check(ref.make([33, 7, 50], [200, 7, 129], 130, 6, 2, 64, 256, seed=35))
+
+
+@gpu
+@pytest.mark.parametrize("rows", [17, 32, 33, 63, 64, 65, 128, 129])
+@pytest.mark.parametrize("P", [1, 63, 64, 65, 127, 190, 700])
+def test_rows_and_ends_of_the_prefix(rows, P):
+    """Row counts around those of the prefix kernel's forms, prefixes that end in
+    the first or second half of a block."""
+    for d in (64, 128):
+        c = ref.make([1] * rows, [1 + 3 * (i % 5) for i in range(rows)], P, 1, 1, d, 16,
+                     seed=rows + P)
+        check(c)

@@ -44,6 +44,7 @@ struct Plan {
     bool halves;          // the two halves of every key block apart
     int slots;            // partial results of all rows
     int line_ctas;
+    int tile_rows;        // query rows of a tile of the line
 };
 
 int ilog2(int x) {
@@ -68,11 +69,12 @@ fa_status check_sizes(int S, int T, int Hq, int Hkv, int d, int page_size, int m
 
 // The prefix's tiles of query rows, and the splits that the workspace has room
 // for.
-Plan plan_rows(int T, int G, int Hkv, int d, int prefix_len) {
+Plan plan_rows(int T, int G, int Hkv, int d, int prefix_len, int max_new) {
     Plan pl{};
     const long long rows = static_cast<long long>(T) * G;
     pl.prefix_in_line = prefix_len > 0 && rows <= kLinePrefixRows;
     pl.tiles = rows > 128 ? 2 : 1;
+    pl.tile_rows = static_cast<long long>(max_new) * G <= 8 ? 8 : 16;
     pl.halves = d == 64 && rows <= kHalvesRows;
     pl.row_tiles = static_cast<int>((rows + 128 * pl.tiles - 1) / (128 * pl.tiles));
     const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
@@ -92,18 +94,19 @@ int prefix_slots(const Plan& pl) {
 int line_ctas(const Plan& pl, int S, int G, int Hkv, int d, int page_size, int max_pages,
               int prefix_len, int max_new, int sm_count) {
     const double cap = (static_cast<long long>(max_pages) * page_size + 63) / 64;
-    const long long tiles = (static_cast<long long>(max_new) * G + 15) / 16;
+    const long long tiles =
+        (static_cast<long long>(max_new) * G + pl.tile_rows - 1) / pl.tile_rows;
     const double blocks = (static_cast<double>(S) * tiles * cap +
                            (pl.prefix_in_line ? (prefix_len + 63) / 64 : 0)) * Hkv;
     const long long per_sm =
-        d == 64 ? fa::OwnTraits<64>::MIN_CTAS : fa::OwnTraits<128>::MIN_CTAS;
+        d == 64 ? fa::OwnTraits<64, 16>::MIN_CTAS : fa::OwnTraits<128, 16>::MIN_CTAS;
     const long long ctas = std::min<long long>(kMaxLineCtas, per_sm * sm_count);
     return blocks < ctas ? static_cast<int>(blocks) : static_cast<int>(ctas);
 }
 
 Plan make_plan(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages, int prefix_len,
                int max_new, int sm_count) {
-    Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len);
+    Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len, max_new);
     pl.line_ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
                              sm_count);
     if (pl.prefix_splits > 0) {
@@ -146,10 +149,11 @@ bool prepare_prefix() {
            cudaFuncGetAttributes(&attr, fa::fa_prefix_kernel<D, TILES, HALVES>) == cudaSuccess &&
            attr.numRegs * T::NUM_THREADS >= T::REG_BUDGET;
 }
-template <int D>
+template <int D, int NR>
 bool prepare_own() {
-    return cudaFuncSetAttribute(fa::fa_own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                fa::OwnTraits<D>::SMEM_BYTES) == cudaSuccess;
+    return cudaFuncSetAttribute(fa::fa_own_kernel<D, NR>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                fa::OwnTraits<D, NR>::SMEM_BYTES) == cudaSuccess;
 }
 
 struct Ready {
@@ -163,7 +167,8 @@ bool prepare(int dev) {
         g_ready[dev].ok = prepare_prefix<64, 1, true>() && prepare_prefix<64, 1, false>() &&
                           prepare_prefix<64, 2, false>() && prepare_prefix<128, 1, false>() &&
                           prepare_prefix<128, 2, false>() &&
-                          prepare_own<64>() && prepare_own<128>();
+                          prepare_own<64, 8>() && prepare_own<64, 16>() &&
+                          prepare_own<128, 8>() && prepare_own<128, 16>();
     });
     return g_ready[dev].ok;
 }
@@ -186,8 +191,11 @@ cudaError_t launch_all(const Plan& pl, const CUtensorMap& mk, const CUtensorMap&
                                   fa::PrefixTraits<D, 1>::SMEM_BYTES, s, mk, mv, mp, prm);
         if (e != cudaSuccess) return e;
     }
-    e = launch_overlapped(fa::fa_own_kernel<D>, dim3(pl.line_ctas), fa::OwnTraits<D>::THREADS,
-                          fa::OwnTraits<D>::SMEM_BYTES, s, mk, mv, prm);
+    e = launch_overlapped(
+        pl.tile_rows == 8 ? fa::fa_own_kernel<D, 8> : fa::fa_own_kernel<D, 16>,
+        dim3(pl.line_ctas), fa::OwnTraits<D, 16>::THREADS,
+        pl.tile_rows == 8 ? fa::OwnTraits<D, 8>::SMEM_BYTES : fa::OwnTraits<D, 16>::SMEM_BYTES, s,
+        mk, mv, prm);
     if (e != cudaSuccess) return e;
     const int rows = prm.T * prm.Hq;
     return rows <= kWideMergeRows
@@ -206,7 +214,7 @@ size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d, int page_si
         T == 0)
         return 0;
     // Enough for any SM count: the splits are bounded by the sizes alone.
-    const Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len);
+    const Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len, max_new);
     const int ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
                                kMaxLineCtas);
     const size_t slots = prefix_len == 0 ? 0 : 1 + prefix_slots(pl);
@@ -292,6 +300,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
     prm.prefix_in_line = pl.prefix_in_line;
     prm.slots = pl.slots;
     prm.line_ctas = pl.line_ctas;
+    prm.tile_rows = pl.tile_rows;
     prm.scale_log2 = sl2;
 
     const long long planes = static_cast<long long>(num_pages) * Hkv;

@@ -63,6 +63,7 @@ struct PagedParams {
     int prefix_slots;         // partial results of the prefix: splits, or twice that (HALVES)
     int prefix_in_line;       // the prefix is one more sequence of the line
     int slots, line_ctas;
+    int tile_rows;            // query rows of a tile of the line, 8 or 16
     float scale_log2;         // scale * log2(e)
 };
 
@@ -70,6 +71,7 @@ struct PagedParams {
 // beside its keys, in blocks: reading Q, joining the warps, writing.
 constexpr int kLineMinBlocks = 2;
 constexpr int kLineTileBlocks = 2;
+constexpr int kPieceRows = 16;  // rows of a CTA's part of a tile, in the workspace
 
 // Plane of (page, head) in the page tensors' maps.  A page out of range is
 // reported and mapped behind the tensor, where TMA fills with zeros.
@@ -535,9 +537,9 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
 
 // ------------------------------------------------------------------ own rows
 
-template <int D>
+template <int D, int NR>
 struct OwnTraits {
-    static constexpr int ROWS = 16;  // query rows per tile (one mma tile)
+    static constexpr int ROWS = NR;  // query rows per tile
     static constexpr int BK = 64;    // keys per stage, 16 per warp
     static constexpr int NCW = 4;    // consumer warps
     static constexpr int CHUNKS = D / 64;
@@ -582,7 +584,7 @@ struct LineSeq {
             len = static_cast<int>(
                 max(0ll, min(static_cast<long long>(p.kv_len[s]), cap)));
         }
-        tiles = static_cast<int>((static_cast<long long>(n) * p.G + 15) / 16);
+        tiles = static_cast<int>((static_cast<long long>(n) * p.G + p.tile_rows - 1) / p.tile_rows);
         blocks = max(1, (len + 63) / 64);  // a tile without keys still has to be written
     }
     __device__ __forceinline__ long long size(const PagedParams& p) const {
@@ -635,7 +637,7 @@ struct LineWalk {
     __device__ __forceinline__ int2 keys(const PagedParams& p) const {
         int seen = seq.len;
         if (s < p.S) {
-            const int last = (min((rt + 1) * 16, seq.n * p.G) - 1) / p.G;
+            const int last = (min((rt + 1) * p.tile_rows, seq.n * p.G) - 1) / p.G;
             seen = max(0, min(seq.len, seq.len - seq.n + last + 1));
         }
         const int beg = min(b0 * 64, seen);
@@ -710,6 +712,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// An 8 x 8 matrix of bf16, two values of a row in each lane, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // Either bf16 of a pair is an infinity or a NaN.
 __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -745,6 +754,28 @@ __device__ __noinline__ void add_visible_row(const uint8_t* v, int r, int col, u
         }
     }
 }
+// The same for the transposed products: o = values col and col + 8 of the two
+// rows whose weights for key e of eight lie in lane 4 e + cq, packed in w0 (the
+// first eight keys) and w1.
+template <int CHUNK_BYTES>
+__device__ __noinline__ void add_visible8(const uint8_t* v, int r, int col, uint32_t w0,
+                                          uint32_t w1, int j0, int end0, int end1,
+                                          float (&o)[4]) {
+#pragma unroll 1
+    for (int e = 0; e < 16; ++e) {
+        const uint32_t w =
+            __shfl_sync(0xffffffffu, e < 8 ? w0 : w1, ((e & 7) << 2) | (threadIdx.x & 3));
+        const float p0 = __uint_as_float(w << 16), p1 = __uint_as_float(w & 0xffff0000u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = col + 8 * h;
+            const float x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                v + (c >> 6) * CHUNK_BYTES + sw128_offset(r + e, (c & 63) >> 3) + (c & 7) * 2));
+            if (j0 + e < end0) o[2 * h] += p0 * x;
+            if (j0 + e < end1) o[2 * h + 1] += p1 * x;
+        }
+    }
+}
 template <int CHUNK_BYTES>
 __device__ __forceinline__ void add_visible(const uint8_t* v, int r, int col,
                                             const uint32_t (&pa)[4], const int (&lim)[2], int j0,
@@ -775,11 +806,18 @@ __device__ __forceinline__ void add_visible(const uint8_t* v, int r, int col,
 // lengths, page table and first stages come in one after another, and 3.3 us a
 // tile beside its keys: 64 sequences of 512 keys on average, 8 heads of 128:
 // 39 us for 134 MB.
-template <int D>
-__global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
+//
+// Up to 8 rows (NR = 8) the products are transposed: S^T = K Q^T and O^T =
+// V^T P^T have the keys, or the head's values, along the 16 rows of an mma and
+// the queries along its 8 columns, so that none of it multiplies padding: half
+// the MMAs and half the registers for Q and O.  P^T is moved from one operand
+// layout to the other by movmatrix, and the rows' maxima are looked at by a
+// vote, and reduced only when one has risen.
+template <int D, int NR>
+__global__ void __launch_bounds__(OwnTraits<D, NR>::THREADS, OwnTraits<D, NR>::MIN_CTAS)
     fa_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const PagedParams p) {
-    using T = OwnTraits<D>;
+    using T = OwnTraits<D, NR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::BAR_OFF);
@@ -905,13 +943,13 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
         const long long part0 =
             whole ? (static_cast<long long>(prefix ? 0 : p.slots - 1) * p.Hkv + head) * p.R +
                         static_cast<long long>(start) * p.G + r0
-                  : p.piece_row + (2ll * blockIdx.x + (first ? 0 : 1)) * T::ROWS;
+                  : p.piece_row + (2ll * blockIdx.x + (first ? 0 : 1)) * kPieceRows;
         if (walk.b0 == 0 && threadIdx.x < T::ROWS && r0 + static_cast<int>(threadIdx.x) < rows) {
             // The tile's later blocks are the next CTAs', `quota` for each.
             const int rest = seq.blocks - walk.b1;
             const int2 d = make_int2(
                 rest <= 0 ? 1 : 2 + static_cast<int>(quotient(rest - 1, quota)),
-                (2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1)) * T::ROWS + threadIdx.x);
+                (2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1)) * kPieceRows + threadIdx.x);
             p.pieces[(static_cast<long long>(prefix) * p.Hkv + head) * p.R +
                      static_cast<long long>(start) * p.G + r0 + threadIdx.x] = d;
         }
@@ -928,151 +966,319 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
             }
             continue;
         }
-        uint32_t qa[D / 16][4];
-        int lim[2];  // last visible key of rows rq and rq + 8
-        const int lim0 = prefix ? len : len - n + r0 / p.G;  // and of the tile's first row
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = r0 + rq + 8 * x;
-            lim[x] = r >= rows ? -1 : prefix ? len - 1 : min(len, len - n + r / p.G + 1) - 1;
-            const __nv_bfloat16* src = p.q + (r < rows ? out_row(rq + 8 * x) : 0) * D + 2 * cq;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                qa[k][x] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
-                qa[k][x + 2] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
-            }
-        }
-        float o[D / 8][4];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
-
         int slot = 0;
-        for (int j = 0; j < nblk; ++j, ++done) {
-            slot = done % T::NSTAGE;
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (done / T::NSTAGE) & 1, st));
-            if (!ok) break;
-            const uint32_t kt = smem_u32(smem + slot * T::STAGE_BYTES);
-            const int j0 = kbeg + j * T::BK + 16 * warp;  // the warp's first key
-            if (j0 < kend) {
-                float sc[2][4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+        float* red;
+        const int lim0 = prefix ? len : len - n + r0 / p.G;  // last key of the tile's first row
+        // Last visible key of row i of the tile.
+        auto last_key = [&](int i) {
+            const int r = r0 + i;
+            return r >= rows ? -1 : prefix ? len - 1 : min(len, len - n + r / p.G + 1) - 1;
+        };
+        if constexpr (NR == 8) {
+            // This thread's scores: keys rq and rq + 8, rows 2 cq and 2 cq + 1.
+            const int lim[2] = {last_key(2 * cq), last_key(2 * cq + 1)};
+            uint32_t qb[D / 16][2];
+            {
+                const bool real = r0 + rq < rows;
+                const __nv_bfloat16* src = p.q + (real ? out_row(rq) : 0) * D + 2 * cq;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const int u = 2 * k + unit_k;
-                    uint32_t b[4];
-                    ldsm4(kt + (u >> 3) * T::CHUNK_BYTES + sw128_offset(key_k, u & 7), b);
-                    mma16816(sc[0], qa[k], b[0], b[1]);
-                    mma16816(sc[1], qa[k], b[2], b[3]);
+                    qb[k][0] = real ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+                    qb[k][1] = real ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
                 }
-                // Online softmax of rows rq and rq + 8 over the warp's 16 keys.
-                uint32_t pa[4];
+            }
+            float o[D / 16][4];  // values 16 i + rq and + 8 of the two rows
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float v[4];
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
+            const int key_a = 16 * warp + (lane & 15), unit_a = lane >> 4;
+            const int key_t = 16 * warp + (lane & 7) + ((lane >> 4) << 3), unit_t = (lane >> 3) & 1;
+
+            for (int j = 0; j < nblk; ++j, ++done) {
+                slot = done % T::NSTAGE;
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (done / T::NSTAGE) & 1, st));
+                if (!ok) break;
+                const uint32_t kt = smem_u32(smem + slot * T::STAGE_BYTES);
+                const int j0 = kbeg + j * T::BK + 16 * warp;  // the warp's first key
+                if (j0 < kend) {
+                    float sc[2][4];  // two chains of products
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = j0 + 8 * i + 2 * cq + e;
-                            v[2 * i + e] = key < kend && key <= lim[x]
-                                               ? sc[i][2 * x + e] * p.scale_log2
-                                               : -INFINITY;
-                        }
-                    float bm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                    if (bm > m[x] + 8.f) {
-                        const float alpha = ex2_approx(m[x] - bm);  // 0 while m = -inf
-                        l[x] *= alpha;
-                        lr[x] *= alpha;
+                        for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < D / 8; ++i) {
-                            o[i][2 * x] *= alpha;
-                            o[i][2 * x + 1] *= alpha;
-                        }
-                        m[x] = bm;
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int u = 2 * k + unit_a;
+                        uint32_t a[4];
+                        ldsm4(kt + (u >> 3) * T::CHUNK_BYTES + sw128_offset(key_a, u & 7), a);
+                        mma16816(sc[k & 1], a, qb[k][0], qb[k][1]);
                     }
-                    const float mm = m[x] == -INFINITY ? 0.f : m[x];
+                    float v[2][2];  // [row][key]
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float p0 = ex2_approx(v[2 * i] - mm);
-                        const float p1 = ex2_approx(v[2 * i + 1] - mm);
-                        l[x] += p0 + p1;
-                        pa[2 * i + x] = pack_bf16x2(p0, p1);
-                        float a = 0.f, b = 0.f;
-                        add_bf16x2_to_f32(pa[2 * i + x], a, b);
-                        lr[x] += a + b;
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) v[x][y] = sc[0][2 * y + x] + sc[1][2 * y + x];
+                    if (j0 + 15 > lim0 || j0 + 16 > kend) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int key = j0 + rq + 8 * y;
+                                if (key >= kend || key > lim[x]) v[x][y] = -INFINITY;
+                            }
+                    }
+                    float bm[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) bm[x] = fmaxf(v[x][0], v[x][1]) * p.scale_log2;
+                    if (__any_sync(0xffffffffu, bm[0] > m[0] + 8.f || bm[1] > m[1] + 8.f)) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1)
+                                bm[x] = fmaxf(bm[x], __shfl_xor_sync(0xffffffffu, bm[x], d));
+                            if (bm[x] > m[x] + 8.f) {
+                                const float alpha = ex2_approx(m[x] - bm[x]);  // 0 while m = -inf
+                                l[x] *= alpha;
+                                lr[x] *= alpha;
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    o[i][x] *= alpha;
+                                    o[i][2 + x] *= alpha;
+                                }
+                                m[x] = bm[x];
+                            }
+                        }
+                    }
+                    const float mm[2] = {m[0] == -INFINITY ? 0.f : m[0],
+                                         m[1] == -INFINITY ? 0.f : m[1]};
+                    uint32_t w[2], pb[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float p0 = ex2_approx(fmaf(v[0][y], p.scale_log2, -mm[0]));
+                        const float p1 = ex2_approx(fmaf(v[1][y], p.scale_log2, -mm[1]));
+                        l[0] += p0;
+                        l[1] += p1;
+                        w[y] = pack_bf16x2(p0, p1);
+                        add_bf16x2_to_f32(w[y], lr[0], lr[1]);
+                        pb[y] = transpose8x8(w[y]);
+                    }
+                    // Keys 2cq, 2cq + 1 (pb[0]) and 2cq + 8, 2cq + 9 (pb[1]) behind
+                    // the last one: their values count as zeros.
+                    const int left = kend - j0;
+                    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                    if (left < 16) {
+                        keep0 = (2 * cq < left ? 0xffffu : 0u) |
+                                (2 * cq + 1 < left ? 0xffff0000u : 0u);
+                        keep1 = (2 * cq + 8 < left ? 0xffffu : 0u) |
+                                (2 * cq + 9 < left ? 0xffff0000u : 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int u = 2 * i + unit_t;
+                        uint32_t a[4];
+                        ldsm4t(kt + T::TILE_BYTES + (u >> 3) * T::CHUNK_BYTES +
+                                   sw128_offset(key_t, u & 7),
+                               a);
+                        a[0] &= keep0;
+                        a[1] &= keep0;
+                        a[2] &= keep1;
+                        a[3] &= keep1;
+                        // As below: values that are not finite reach only the
+                        // rows that see their key.
+                        if (j0 + 15 > lim0 &&
+                            __any_sync(0xffffffffu, not_finite(a[0]) || not_finite(a[1]) ||
+                                                        not_finite(a[2]) || not_finite(a[3]))) {
+                            float t[4] = {o[i][0], o[i][1], o[i][2], o[i][3]};
+                            add_visible8<T::CHUNK_BYTES>(
+                                smem + slot * T::STAGE_BYTES + T::TILE_BYTES, 16 * warp,
+                                16 * i + rq, w[0], w[1], j0, min(lim[0] + 1, kend),
+                                min(lim[1] + 1, kend), t);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[i][e] = t[e];
+                            continue;
+                        }
+                        mma16816(o[i], a, pb[0], pb[1]);
                     }
                 }
-                // Keys 2cq, 2cq + 1 (b0) and 2cq + 8, 2cq + 9 (b1) behind the
-                // last one: their values count as zeros.
-                const int left = kend - j0;
-                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-                if (left < 16) {
-                    keep0 = (2 * cq < left ? 0xffffu : 0u) | (2 * cq + 1 < left ? 0xffff0000u : 0u);
-                    keep1 = (2 * cq + 8 < left ? 0xffffu : 0u) |
-                            (2 * cq + 9 < left ? 0xffff0000u : 0u);
+                __syncwarp();
+                if (lane == 0 && j + 1 < nblk) mbar_arrive(&empty[slot]);
+            }
+
+            // Row sums over the eight lanes that share a row, then the four
+            // warps' results through the tile's last stage, given back after
+            // that, its 8-float units swapped by row pair.
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
+                    lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], d);
+                }
+            red = reinterpret_cast<float*>(smem + slot * T::STAGE_BYTES);  // [NCW][ROWS][D]
+            named_bar_sync(1, T::NCW * 32);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = warp * T::ROWS + 2 * cq + x;
+                if (rq == 0) {
+                    red_ml[3 * r] = m[x];
+                    red_ml[3 * r + 1] = l[x];
+                    red_ml[3 * r + 2] = lr[x];
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const int u = 2 * i + unit_v;
-                    uint32_t b[4];
-                    ldsm4t(kt + T::TILE_BYTES + (u >> 3) * T::CHUNK_BYTES +
-                               sw128_offset(key_v, u & 7),
-                           b);
-                    b[0] &= keep0;
-                    b[1] &= keep1;
-                    b[2] &= keep0;
-                    b[3] &= keep1;
-                    // A key that some rows do not see must not reach them, and a
-                    // weight of zero times infinity would: such values are added
-                    // row by row.
-                    if (j0 + 15 > lim0 &&
-                        __any_sync(0xffffffffu, not_finite(b[0]) || not_finite(b[1]) ||
-                                                    not_finite(b[2]) || not_finite(b[3]))) {
-                        add_visible<T::CHUNK_BYTES>(smem + slot * T::STAGE_BYTES + T::TILE_BYTES,
-                                                    16 * warp, 16 * i + 2 * cq, pa, lim, j0, kend,
-                                                    o[2 * i], o[2 * i + 1]);
-                        continue;
-                    }
-                    mma16816(o[2 * i], pa, b[0], b[1]);
-                    mma16816(o[2 * i + 1], pa, b[2], b[3]);
+                    red[r * D + 8 * ((2 * i) ^ cq) + rq] = o[i][x];
+                    red[r * D + 8 * ((2 * i + 1) ^ cq) + rq] = o[i][2 + x];
                 }
             }
-            __syncwarp();
-            if (lane == 0 && j + 1 < nblk) mbar_arrive(&empty[slot]);
-        }
-
-        // Row sums over the four lanes of a row, then the four warps' results
-        // through the tile's last stage, which is given back only after that.  Its
-        // 8-float units are swapped by row, so that the writes meet every bank.
+        } else {
+            uint32_t qa[D / 16][4];
+            int lim[2];  // last visible key of rows rq and rq + 8
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x) {
+                const int r = r0 + rq + 8 * x;
+                lim[x] = last_key(rq + 8 * x);
+                const __nv_bfloat16* src = p.q + (r < rows ? out_row(rq + 8 * x) : 0) * D + 2 * cq;
 #pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
-                l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
-                lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], d);
+                for (int k = 0; k < D / 16; ++k) {
+                    qa[k][x] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+                    qa[k][x + 2] =
+                        r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+                }
             }
-        float* red = reinterpret_cast<float*>(smem + slot * T::STAGE_BYTES);  // [NCW][ROWS][D]
-        named_bar_sync(1, T::NCW * 32);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = warp * T::ROWS + rq + 8 * x;
-            if (cq == 0) {
-                red_ml[3 * r] = m[x];
-                red_ml[3 * r + 1] = l[x];
-                red_ml[3 * r + 2] = lr[x];
-            }
+            float o[D / 8][4];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2*>(red + r * D + 8 * (i ^ (rq & 7)) + 2 * cq) =
-                    make_float2(o[i][2 * x], o[i][2 * x + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
+
+            for (int j = 0; j < nblk; ++j, ++done) {
+                slot = done % T::NSTAGE;
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (done / T::NSTAGE) & 1, st));
+                if (!ok) break;
+                const uint32_t kt = smem_u32(smem + slot * T::STAGE_BYTES);
+                const int j0 = kbeg + j * T::BK + 16 * warp;  // the warp's first key
+                if (j0 < kend) {
+                    float sc[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int u = 2 * k + unit_k;
+                        uint32_t b[4];
+                        ldsm4(kt + (u >> 3) * T::CHUNK_BYTES + sw128_offset(key_k, u & 7), b);
+                        mma16816(sc[0], qa[k], b[0], b[1]);
+                        mma16816(sc[1], qa[k], b[2], b[3]);
+                    }
+                    // Online softmax of rows rq and rq + 8 over the warp's 16 keys.
+                    uint32_t pa[4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float v[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = j0 + 8 * i + 2 * cq + e;
+                                v[2 * i + e] = key < kend && key <= lim[x]
+                                                   ? sc[i][2 * x + e] * p.scale_log2
+                                                   : -INFINITY;
+                            }
+                        float bm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                        if (bm > m[x] + 8.f) {
+                            const float alpha = ex2_approx(m[x] - bm);  // 0 while m = -inf
+                            l[x] *= alpha;
+                            lr[x] *= alpha;
+#pragma unroll
+                            for (int i = 0; i < D / 8; ++i) {
+                                o[i][2 * x] *= alpha;
+                                o[i][2 * x + 1] *= alpha;
+                            }
+                            m[x] = bm;
+                        }
+                        const float mm = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float p0 = ex2_approx(v[2 * i] - mm);
+                            const float p1 = ex2_approx(v[2 * i + 1] - mm);
+                            l[x] += p0 + p1;
+                            pa[2 * i + x] = pack_bf16x2(p0, p1);
+                            float a = 0.f, b = 0.f;
+                            add_bf16x2_to_f32(pa[2 * i + x], a, b);
+                            lr[x] += a + b;
+                        }
+                    }
+                    // Keys 2cq, 2cq + 1 (b0) and 2cq + 8, 2cq + 9 (b1) behind the
+                    // last one: their values count as zeros.
+                    const int left = kend - j0;
+                    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                    if (left < 16) {
+                        keep0 = (2 * cq < left ? 0xffffu : 0u) |
+                                (2 * cq + 1 < left ? 0xffff0000u : 0u);
+                        keep1 = (2 * cq + 8 < left ? 0xffffu : 0u) |
+                                (2 * cq + 9 < left ? 0xffff0000u : 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int u = 2 * i + unit_v;
+                        uint32_t b[4];
+                        ldsm4t(kt + T::TILE_BYTES + (u >> 3) * T::CHUNK_BYTES +
+                                   sw128_offset(key_v, u & 7),
+                               b);
+                        b[0] &= keep0;
+                        b[1] &= keep1;
+                        b[2] &= keep0;
+                        b[3] &= keep1;
+                        // A key that some rows do not see must not reach them, and a
+                        // weight of zero times infinity would: such values are added
+                        // row by row.
+                        if (j0 + 15 > lim0 &&
+                            __any_sync(0xffffffffu, not_finite(b[0]) || not_finite(b[1]) ||
+                                                        not_finite(b[2]) || not_finite(b[3]))) {
+                            add_visible<T::CHUNK_BYTES>(
+                                smem + slot * T::STAGE_BYTES + T::TILE_BYTES, 16 * warp,
+                                16 * i + 2 * cq, pa, lim, j0, kend, o[2 * i], o[2 * i + 1]);
+                            continue;
+                        }
+                        mma16816(o[2 * i], pa, b[0], b[1]);
+                        mma16816(o[2 * i + 1], pa, b[2], b[3]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0 && j + 1 < nblk) mbar_arrive(&empty[slot]);
+            }
+
+            // Row sums over the four lanes of a row, then the four warps' results
+            // through the tile's last stage, which is given back only after that.  Its
+            // 8-float units are swapped by row, so that the writes meet every bank.
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) {
+                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
+                    lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], d);
+                }
+            red = reinterpret_cast<float*>(smem + slot * T::STAGE_BYTES);  // [NCW][ROWS][D]
+            named_bar_sync(1, T::NCW * 32);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = warp * T::ROWS + rq + 8 * x;
+                if (cq == 0) {
+                    red_ml[3 * r] = m[x];
+                    red_ml[3 * r + 1] = l[x];
+                    red_ml[3 * r + 2] = lr[x];
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *reinterpret_cast<float2*>(red + r * D + 8 * (i ^ (rq & 7)) + 2 * cq) =
+                        make_float2(o[i][2 * x], o[i][2 * x + 1]);
+            }
         }
         // One answer for all warps, so that none waits here for one that gave up.
         if (threadIdx.x == 0) *carry_on = *abort_flag == 0;
@@ -1093,7 +1299,8 @@ __global__ void __launch_bounds__(OwnTraits<D>::THREADS, OwnTraits<D>::MIN_CTAS)
                 // NaN has m = -inf too, and its NaN must reach the row.
                 const float f = ml[0] == -INFINITY ? 1.f : ex2_approx(ml[0] - M);
                 const float4 x = *reinterpret_cast<const float4*>(
-                    red + (w * T::ROWS + r) * D + 8 * ((e4 >> 3) ^ (r & 7)) + (e4 & 7));
+                    red + (w * T::ROWS + r) * D +
+                    8 * ((e4 >> 3) ^ (NR == 8 ? (r >> 1) & 3 : r & 7)) + (e4 & 7));
                 L += f * ml[1];
                 Lr += f * ml[2];
                 a.x += f * x.x;

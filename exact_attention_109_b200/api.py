@@ -640,7 +640,8 @@ def attention_paged(q, k_pages, v_pages, block_table, seq_start, kv_len, scale: 
     [num_pages, Hkv, page_size, d], found through ``block_table``
     [S, max_pages].  ``seq_start`` [S+1] holds each sequence's first token; the
     three are int32.  max_new: the most new tokens any sequence has (default:
-    T); more are reported as FA_ERR_INDEX.  Rows that belong to no sequence are
+    T; a tight bound lets few rows run in smaller tiles); more are reported as
+    FA_ERR_INDEX.  Rows that belong to no sequence are
     not written."""
     return _call(_native().attention_paged, stream, q, q, k_pages, v_pages, block_table,
                  seq_start, kv_len, scale, prefix_pages, prefix_len, max_new, out, lse, workspace)

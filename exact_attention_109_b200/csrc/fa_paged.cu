@@ -25,6 +25,11 @@ constexpr int kMaxLineCtas = 444;
 // 16.7 / 20.1 / 71.5 against 21.0 / 24.5 / 69.7.  32 rows: 44.9 in the line
 // against 39.8 (16384 keys of 128).
 constexpr int kLinePrefixRows = 16;
+// Rows of a sequence and key head up to which the line's tiles have 8: 8 rows of
+// 16 sequences of 4096 keys, 4 heads of 128 / 64: 33.9 / 22.6 us, 35.3 / 23.6 in
+// tiles of 16; 12 rows, which read their keys twice in tiles of 8: 53.2 / 29.4
+// and 39.1 / 23.8.
+constexpr int kSmallTileRows = 8;
 // Query rows of a key head up to which the prefix kernel takes them twice, with
 // heads of 64: 20 rows of 32 heads behind 4096 / 16384 / 65536 keys 31.6 / 50.7 /
 // 123 us, 32.7 / 56.4 / 143 with two idle softmax warps.  Heads of 128 are bound
@@ -74,7 +79,7 @@ Plan plan_rows(int T, int G, int Hkv, int d, int prefix_len, int max_new) {
     const long long rows = static_cast<long long>(T) * G;
     pl.prefix_in_line = prefix_len > 0 && rows <= kLinePrefixRows;
     pl.tiles = rows > 128 ? 2 : 1;
-    pl.tile_rows = static_cast<long long>(max_new) * G <= 8 ? 8 : 16;
+    pl.tile_rows = static_cast<long long>(max_new) * G <= kSmallTileRows ? 8 : 16;
     pl.halves = d == 64 && rows <= kHalvesRows;
     pl.row_tiles = static_cast<int>((rows + 128 * pl.tiles - 1) / (128 * pl.tiles));
     const long long units = static_cast<long long>(Hkv) * pl.row_tiles;

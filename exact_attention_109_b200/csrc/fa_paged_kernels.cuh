@@ -15,7 +15,7 @@
 //    SM streams.
 //  * Own rows (fa_own_kernel).  One sequence's keys serve only its own n * G
 //    rows (a handful), so this part is bound by reading the cache; a 128-row
-//    tile would be mostly padding.  Warps use 16-row mma.sync tiles on keys
+//    tile would be mostly padding.  Warps use 8- or 16-row mma.sync tiles on keys
 //    streamed through shared memory by TMA.  The key blocks of all sequences
 //    and heads form one line that is cut into equal pieces, one per CTA, so
 //    ragged lengths leave no SM idle and the loads never stop between them.
@@ -798,21 +798,20 @@ __device__ __forceinline__ void add_visible(const uint8_t* v, int r, int col,
 // 64-key stage and keeps its own running maximum, sum and O; they are merged
 // at the end of a tile's share.
 //
-// Bound by HBM: with 4 * D bytes a key against 16 rows the mma.sync tiles need
-// less time than the reads (a 64-key stage of 128 takes 1.25 us of a CTA's
-// chain, its share of HBM 1.46 us with two CTAs an SM).  16 sequences of 8192
-// keys, 16 heads of 128: 164 to 171 us for 1.07 GB (96 to 100 % of the measured
-// copy bandwidth).  Ragged short sequences pay the first 6 us, in which the
-// lengths, page table and first stages come in one after another, and 3.3 us a
-// tile beside its keys: 64 sequences of 512 keys on average, 8 heads of 128:
-// 39 us for 134 MB.
+// Bound by HBM where sequences are long: 16 of 8192 keys, 16 heads of 128: 164
+// to 169 us for 1.07 GB (97 to 100 % of the measured copy bandwidth).  Ragged
+// short sequences pay the first 6 us, in which the lengths, page table and first
+// stages come in one after another, and a tile's fixed part (its rows, joining
+// the warps, writing); 64 sequences of 512 keys on average, 8 heads of 128,
+// behind a prefix: 26 us for 134 MB.
 //
 // Up to 8 rows (NR = 8) the products are transposed: S^T = K Q^T and O^T =
 // V^T P^T have the keys, or the head's values, along the 16 rows of an mma and
 // the queries along its 8 columns, so that none of it multiplies padding: half
 // the MMAs and half the registers for Q and O.  P^T is moved from one operand
 // layout to the other by movmatrix, and the rows' maxima are looked at by a
-// vote, and reduced only when one has risen.
+// vote, and reduced only when one has risen.  (16 rows: 1.25 us for a 64-key
+// stage of a CTA, 3.3 us for a tile; that case 30 us.)
 template <int D, int NR>
 __global__ void __launch_bounds__(OwnTraits<D, NR>::THREADS, OwnTraits<D, NR>::MIN_CTAS)
     fa_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,

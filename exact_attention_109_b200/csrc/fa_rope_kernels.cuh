@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
         if (active) {
             const int s = sequence_of(dst.seq_start, dst.S, t);
             const int have = dst.cache_len[s];
-            const long long at = static_cast<long long>(have) + (t - dst.seq_start[s]);
+            // In 64 bits: a start far below 0, which is reported below, must not
+            // turn the key's index, and with it the table's, negative.
+            const long long at = static_cast<long long>(have) + t - dst.seq_start[s];
             const long long slot = at >> dst.page_shift;
             pos = at + dst.pos_offset;
             if (have >= 0 && slot < dst.max_pages) {

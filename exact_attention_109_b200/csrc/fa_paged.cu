@@ -279,6 +279,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
     prm.seq_start = seq_start;
     prm.kv_len = kv_len;
     prm.prefix_pages = prefix_pages;
+    prm.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
     prm.o = static_cast<__nv_bfloat16*>(o);
     prm.lse = lse;
     prm.pieces = static_cast<int2*>(workspace);

@@ -41,6 +41,7 @@ struct PagedParams {
     const int* seq_start;     // [S + 1]
     const int* kv_len;        // [S]
     const int* prefix_pages;  // [ceil(prefix_len / page)]
+    const __nv_bfloat16* v_pages;  // [num_pages][Hkv][page][D], for not_finite_values
     __nv_bfloat16* o;         // [T][Hq][D]
     float* lse;               // [T][Hq], natural log
     // Partial results, normalised, with their log-sum-exp (base 2; -inf:
@@ -118,6 +119,26 @@ struct PrefixTraits {
     static constexpr float TAU = 8.0f;  // deferred-rescale threshold (log2 units)
 };
 
+// Keys [key, kend) of the prefix, heads of 64: the sums of their values that are
+// not finite, of columns 2 * lane and 2 * lane + 1 (0 where all are).
+__device__ __noinline__ float2 not_finite_values(const __nv_bfloat16* v_pages, const int* pages,
+                                                 int num_pages, int Hkv, int head, int page_shift,
+                                                 int key, int kend) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (; key < kend; ++key) {
+        const int page = pages[key >> page_shift];
+        if (page < 0 || page >= num_pages) continue;  // reported by the loading warp
+        const long long row = ((static_cast<long long>(page) * Hkv + head) << page_shift) +
+                              (key & ((1 << page_shift) - 1));
+        const uint32_t w =
+            *reinterpret_cast<const uint32_t*>(v_pages + row * 64 + 2 * (threadIdx.x & 31));
+        if ((w & 0x7f80u) == 0x7f80u) sum.x += __uint_as_float(w << 16);
+        if ((w & 0x7f800000u) == 0x7f800000u) sum.y += __uint_as_float(w & 0xffff0000u);
+    }
+    return sum;
+}
+
 // One CTA: 128 * TILES query rows of a key head against one split of the
 // prefix.  Roles as in fa_fwd_kernel: a softmax warpgroup per query tile (one
 // thread per row), a thread that issues the MMAs, a warp that loads; one more
@@ -137,7 +158,12 @@ struct PrefixTraits {
 // HALVES: at most 64 query rows.  They stand in the tile twice, and the two
 // copies take a half of every block's keys each, so that all four softmax warps
 // have work and half as much of it; the copies' results are joined like those
-// of two splits.
+// of two splits.  The value product runs over all keys for both, with weights of
+// zero for the other copy's, and zero times an infinity is NaN: where an output
+// column is NaN at the end, the split's values of that column are looked through
+// again, and what is not finite among them takes its place (an infinity where
+// all have one sign).  In a row of finite scores that is what the definition
+// gives, for either copy: the row meets all of these keys.
 template <int D, int TILES, bool HALVES>
 __global__ void __launch_bounds__(128 * (TILES + 1), 1)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -500,6 +526,24 @@ __global__ void __launch_bounds__(128 * (TILES + 1), 1)
                 uint32_t o[32];
                 tmem_ld32(o_tm + 32u * c, o);
                 tmem_ld_wait();
+                if constexpr (HALVES) {
+                    static_assert(D == 64, "two columns a lane");
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) bad |= isnan(__uint_as_float(o[e]));
+                    // (a row with a NaN score stays NaN: its sum is one)
+                    if (__any_sync(0xffffffffu, bad && !isnan(l))) {
+                        const float2 f =
+                            not_finite_values(p.v_pages, p.prefix_pages, p.num_pages, p.Hkv, head,
+                                              p.page_shift, kbeg, kend);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float x =
+                                __shfl_sync(0xffffffffu, e & 1 ? f.y : f.x, 16 * c + e / 2);
+                            if (isnan(__uint_as_float(o[e]))) o[e] = __float_as_uint(x);
+                        }
+                    }
+                }
                 if (c >= T::CHUNKS) {  // the store that used this buffer has read it
                     if (lane == 0) bulk_wait_group_read<T::CHUNKS - 1>();
                     __syncwarp();

@@ -19,17 +19,25 @@ constexpr int kMaxDevices = 64;
 constexpr long long kMaxPrefixCtas = 512;
 constexpr int kMaxLineCtas = 444;
 // Query rows of a key head for which the prefix joins the line of the sequences:
-// one row tile, so that its keys are still read once, and a launch less.  16
-// sequences, 8 heads of 64, behind 1024 / 4096 / 65536 keys: 12.7 / 14.8 /
-// 43.7 us in the line, 17.1 / 19.4 / 46.7 on the tensor-core path; heads of 128
-// 16.7 / 20.1 / 71.5 against 21.0 / 24.5 / 69.7.  32 rows: 44.9 in the line
-// against 39.8 (16384 keys of 128).
+// a row tile of the line, and a launch less.  12 sequences of one token and 300
+// own keys behind 1024 / 4096 / 16384 / 65536 keys, 16 heads of 64: 18.4 / 21.2 /
+// 30.7 / 64.2 us in the line, 22.8 / 25.5 / 35.8 / 70.5 on the tensor-core path;
+// 16 heads of 128: 24.6 / 28.9 / 45.1 / 110.6 and 27.7 / 32.5 / 47.2 / 105.7.  Four
+// query heads a key head (four sequences, 4 heads of 64) gain from the other
+// path at 16384 alone: 22.5 against 18.5.
 constexpr int kLinePrefixRows = 16;
 // Rows of a sequence and key head up to which the line's tiles have 8: 8 rows of
 // 16 sequences of 4096 keys, 4 heads of 128 / 64: 33.9 / 22.6 us, 35.3 / 23.6 in
 // tiles of 16; 12 rows, which read their keys twice in tiles of 8: 53.2 / 29.4
 // and 39.1 / 23.8.
 constexpr int kSmallTileRows = 8;
+// Keys of a prefix in the line up to which two tiles of 8 rows, the second of
+// which finds the keys in L2, are as good as one of 16 for it and better for the
+// own keys: 16 sequences as above, 16 heads of 128, behind 256 / 1024 / 4096 keys
+// 22.9 / 24.6 / 31.1 us in tiles of 8, 26.6 / 28.7 / 31.6 in tiles of 16; behind
+// 16384 / 65536 keys 68.5 / 196 and 48.2 / 111.  Heads of 64: 18.4 / 20.1 / 22.5
+// and 20.5 / 20.5 / 22.5, 35.5 / 88 and 32.5 / 67.
+constexpr int kTwoTileKeys = 4096;
 // Query rows of a key head up to which the prefix kernel takes them twice, with
 // heads of 64: 20 rows of 32 heads behind 4096 / 16384 / 65536 keys 31.6 / 50.7 /
 // 123 us, 32.7 / 56.4 / 143 with two idle softmax warps.  Heads of 128 are bound
@@ -79,7 +87,10 @@ Plan plan_rows(int T, int G, int Hkv, int d, int prefix_len, int max_new) {
     const long long rows = static_cast<long long>(T) * G;
     pl.prefix_in_line = prefix_len > 0 && rows <= kLinePrefixRows;
     pl.tiles = rows > 128 ? 2 : 1;
-    pl.tile_rows = static_cast<long long>(max_new) * G <= kSmallTileRows ? 8 : 16;
+    // A long prefix in the line is one tile, so that its keys are read once.
+    const long long one_tile = pl.prefix_in_line && prefix_len > kTwoTileKeys ? rows : 0;
+    pl.tile_rows =
+        std::max(static_cast<long long>(max_new) * G, one_tile) <= kSmallTileRows ? 8 : 16;
     pl.halves = d == 64 && rows <= kHalvesRows;
     pl.row_tiles = static_cast<int>((rows + 128 * pl.tiles - 1) / (128 * pl.tiles));
     const long long units = static_cast<long long>(Hkv) * pl.row_tiles;
@@ -96,13 +107,16 @@ int prefix_slots(const Plan& pl) {
 
 // CTAs of the line: as many as are resident, unless the longest line has less
 // work.
-int line_ctas(const Plan& pl, int S, int G, int Hkv, int d, int page_size, int max_pages,
+int line_ctas(const Plan& pl, int S, int T, int G, int Hkv, int d, int page_size, int max_pages,
               int prefix_len, int max_new, int sm_count) {
     const double cap = (static_cast<long long>(max_pages) * page_size + 63) / 64;
-    const long long tiles =
-        (static_cast<long long>(max_new) * G + pl.tile_rows - 1) / pl.tile_rows;
-    const double blocks = (static_cast<double>(S) * tiles * cap +
-                           (pl.prefix_in_line ? (prefix_len + 63) / 64 : 0)) * Hkv;
+    auto tiles = [&](long long rows) {
+        return static_cast<double>((rows + pl.tile_rows - 1) / pl.tile_rows);
+    };
+    const double own = S * tiles(static_cast<long long>(max_new) * G) * cap;
+    const double prefix = pl.prefix_in_line ? tiles(static_cast<long long>(T) * G) *
+                                                  ((prefix_len + 63) / 64) : 0.0;
+    const double blocks = (own + prefix) * Hkv;
     const long long per_sm =
         d == 64 ? fa::OwnTraits<64, 16>::MIN_CTAS : fa::OwnTraits<128, 16>::MIN_CTAS;
     const long long ctas = std::min<long long>(kMaxLineCtas, per_sm * sm_count);
@@ -112,7 +126,7 @@ int line_ctas(const Plan& pl, int S, int G, int Hkv, int d, int page_size, int m
 Plan make_plan(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages, int prefix_len,
                int max_new, int sm_count) {
     Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len, max_new);
-    pl.line_ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
+    pl.line_ctas = line_ctas(pl, S, T, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
                              sm_count);
     if (pl.prefix_splits > 0) {
         // The splits with the fewest waves of CTAs (one per SM), a CTA's time
@@ -220,8 +234,8 @@ size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d, int page_si
         return 0;
     // Enough for any SM count: the splits are bounded by the sizes alone.
     const Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len, max_new);
-    const int ctas = line_ctas(pl, S, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len, max_new,
-                               kMaxLineCtas);
+    const int ctas = line_ctas(pl, S, T, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len,
+                               max_new, kMaxLineCtas);
     const size_t slots = prefix_len == 0 ? 0 : 1 + prefix_slots(pl);
     return table_bytes(T, Hq) + (slots * T * Hq + ctas * 2 * 16) * (d + 1) * sizeof(float);
 }

@@ -19,7 +19,8 @@
 //    streamed through shared memory by TMA.  The key blocks of all sequences
 //    and heads form one line that is cut into equal pieces, one per CTA, so
 //    ragged lengths leave no SM idle and the loads never stop between them.
-//    A prefix that 16 rows or fewer read is one more sequence of this line.
+//    A prefix that 16 rows or fewer read is one more sequence of this line: one
+//    tile of it, or two of 8 rows behind a prefix that L2 holds.
 //  * fa_paged_merge_kernel joins the partial results of a row.
 //
 // A page is [page rows][d] per head, contiguous, so one TMA box of

@@ -477,8 +477,10 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v,
 
 /*
  * fa_fwd_paged -- attention of the packed new tokens over the paged cache,
- * behind an optional prefix that all sequences share and that is read once
- * for the whole batch (the split-KV merge of fa_fwd_decode joins the parts).
+ * behind an optional prefix that all sequences share and that comes from memory
+ * once for the whole batch, not once a sequence; tiles of its query rows that
+ * follow each other read it from L2 (the split-KV merge of fa_fwd_decode joins
+ * the parts).
  *   q         [T,Hq,d] bf16, contiguous.
  *   kv_len    [S] int32: keys of each sequence, its new tokens included
  *             (after fa_paged_append: cache_len + its new tokens).  With n

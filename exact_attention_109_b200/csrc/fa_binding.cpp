@@ -167,6 +167,8 @@ struct NormRope {
         const at::Tensor& t = tensor(rope, "rope");
         if (t.dim() != 3 || t.size(2) != 2)
             fail(PyExc_ValueError, "rope", "expected a [positions, rope_dim / 2, 2] table");
+        // Its pointer would be null, which the C ABI takes for no rotation.
+        if (t.numel() == 0) fail(PyExc_ValueError, "rope", "the table is empty");
         table = static_cast<float*>(exact(t, "rope", t.sizes(), at::kFloat, dev));
         rows = t.size(0);
         width = static_cast<int>(std::min<int64_t>(2 * t.size(1), 1 << 20));

@@ -8,6 +8,7 @@ fallback path, and a missing library raises ``FaError`` on first use.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -545,14 +546,17 @@ def _native():
     counts."""
     global _binding
     if _binding is None:
+        from . import build
         library()
-        try:
-            from . import _fa_binding
-        except ImportError as e:
-            raise FaError(FA_ERR_UNSUPPORTED,
-                          f"_fa_binding not built (run __graft_entry__.build()): {e}") from e
-        _fa_binding.set_status_error(FaError)
-        _binding = _fa_binding
+        path = build.binding_path()
+        if not os.path.exists(path):
+            raise FaError(FA_ERR_UNSUPPORTED, f"{os.path.basename(path)} not built "
+                                              "(run __graft_entry__.build())")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._fa_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_status_error(FaError)
+        _binding = module
     return _binding
 
 

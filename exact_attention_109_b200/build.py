@@ -25,7 +25,6 @@ def headers():
 
 OUT = os.path.join(HERE, "libfa_sm100.so")
 BINDING_SOURCE = os.path.join(HERE, "csrc", "fa_binding.cpp")
-BINDING = os.path.join(HERE, "_fa_binding.so")
 
 
 def nvcc_command(out: str = OUT, extra=()):
@@ -35,7 +34,16 @@ def nvcc_command(out: str = OUT, extra=()):
             "-I", os.path.join(ROOT, "include"), "-o", out, *SOURCES, *extra]
 
 
-def binding_command(out: str = BINDING):
+def binding_path() -> str:
+    """Where the compiled part of the Python binding is: its name holds the torch
+    and the Python that it is built for, whose C++ and C interfaces it calls, so
+    that under others it is built anew and not loaded."""
+    import torch
+    return os.path.join(HERE, f"_fa_binding.torch-{torch.__version__}"
+                              f"{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def binding_command(out: str):
     """The compiled part of the Python binding, against this torch's headers."""
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
@@ -62,8 +70,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or not up_to_date():
         extra = ["-Xptxas", "-v"] if verbose else []
         subprocess.run(nvcc_command(extra=extra), check=True)
-    if force or not up_to_date(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h")]):
-        subprocess.run(binding_command(), check=True)
+    binding = binding_path()
+    if force or not up_to_date(binding, [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h")]):
+        subprocess.run(binding_command(binding), check=True)
     return OUT
 
 

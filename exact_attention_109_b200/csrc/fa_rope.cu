@@ -14,11 +14,11 @@ namespace {
 
 using fa_host::aligned;
 
-// CTAs of the backward kernel at most, and so rows of its dw partials: the two
-// that an SM's registers hold, on each of 148 SMs.
-constexpr int kBwdCtas = 296;
+// CTAs of the backward kernel at most, and so rows of its dw partials in the
+// workspace: two waves of the two that an SM's registers hold, on 148 SMs.
+constexpr int kMaxBwdCtas = 592;
 constexpr long long kMinHeads = 2;    // heads that a CTA takes at least
-constexpr long long kManyHeads = 16;  // from here on, twice as many CTAs take half each:
+constexpr long long kManyHeads = 16;  // from twice that in one wave on, CTAs take half each:
                                       // the second wave evens out the first (16384 tokens of
                                       // 48 heads of 128: 102 -> 100 us)
 // CTAs up to which the heads of a token block are spread over more CTAs: three
@@ -136,8 +136,9 @@ cudaError_t launch_prep_bwd(const fa::HeadRows (&dy)[3], const fa::HeadRows (&x)
     const long long blocks = (static_cast<long long>(p.B) * p.N + TOKENS - 1) / TOKENS;
     const int heads = p.Hq + p.Hkv + (dy[2].p ? p.Hkv : 0);
     const long long units = blocks * heads;
-    long long per_cta = std::max(kMinHeads, (units + kBwdCtas - 1) / kBwdCtas);
-    if (per_cta >= 2 * kManyHeads) per_cta = (per_cta + 1) / 2;
+    constexpr int kWave = kMaxBwdCtas / 2;
+    long long per_cta = std::max(kMinHeads, (units + kWave - 1) / kWave);
+    if (per_cta >= 2 * kManyHeads) per_cta = (per_cta + 1) / 2;  // still no more than two waves
     const int grid = static_cast<int>((units + per_cta - 1) / per_cta);
     const auto kernel =
         p.wq ? fa::fa_prep_bwd_kernel<D, IL, true> : fa::fa_prep_bwd_kernel<D, IL, false>;
@@ -217,7 +218,7 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v, const lon
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
-    return d == 64 || d == 128 ? static_cast<size_t>(2 * kBwdCtas) * 2 * d * sizeof(float) : 0;
+    return d == 64 || d == 128 ? static_cast<size_t>(kMaxBwdCtas) * 2 * d * sizeof(float) : 0;
 }
 
 fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* dv_out,

@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(OwnTraits<D, NR>::THREADS, OwnTraits<D, NR>::M
         tma_prefetch_desc(&tmV);
     }
     // Behind a prefix this grid starts when the prefix's has seen the end of
-    // what came before; alone it waits for that itself.
+    // what came before; alone it waits for that itself (see launch_overlapped).
     if (!p.prefix_splits) grid_dependency_wait();
     grid_launch_dependents();
     // Starts, lengths and counts out of range are reported once.
@@ -1437,6 +1437,8 @@ __global__ void __launch_bounds__(128, 5) fa_paged_merge_kernel(const PagedParam
     const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - 1ll * t * p.Hq);
     const int head = hq / p.G, g = hq - head * p.G;
     grid_launch_dependents();
+    // (Read ahead of the wait: when this grid may start, all that came before the
+    // call has ended; see launch_overlapped.)
     const bool mine = row < static_cast<long long>(p.T) * p.Hq && t >= p.seq_start[0] &&
                       t < p.seq_start[p.S];  // else no sequence's row
     const long long plane_row = static_cast<long long>(head) * p.R +

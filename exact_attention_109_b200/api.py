@@ -599,7 +599,10 @@ def qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-6, 
     strides with the last dimension contiguous (such as parts of one
     projection): RMS norm of each row with the weights (both or neither, bf16
     or fp32) and rotation by the table ``rope`` (see ``rope_table``) at
-    ``positions`` [B,N] int32 (default: 0 .. N-1)."""
+    ``positions`` [B,N] int32 (default: 0 .. N-1).  ``attention_forward``,
+    ``attention_backward`` and ``attention_decode`` take the outputs with
+    Hkv = Hq; for fewer key heads repeat k_out and v_out (and sum the gradients
+    over the repeats): ``k_out.repeat_interleave(Hq // Hkv, 1)``."""
     return _call(_native().qk_norm_rope, stream, q, q, k, v, q_weight, k_weight, eps, rope,
                  positions, interleaved, q_out, k_out, v_out)
 

@@ -364,7 +364,7 @@ fa_status fa_decode_split_plan(int B, int H, int Nq, int Nk, int d,
 /*
  * Between a projection and attention: the RMS norm of every head's query and
  * key row, the rotation of positions, and the move from the projection's
- * token-major rows to the layout the attention entry points read.
+ * token-major rows to head-major ones, or into the pages of a cache.
  *
  * For a row x of d values, with u = x * (mean(x^2) + eps)^(-1/2) * weight,
  * every pair (a, b) among the first rope_dim values of u is turned by its
@@ -381,8 +381,8 @@ fa_status fa_decode_split_plan(int B, int H, int Nq, int Nk, int d,
  *             position p (as fa_rope_table writes them), or NULL: no
  *             rotation.  rope_dim is a multiple of 16, 16 .. d; values beyond
  *             it are not turned.
- *   Hq is a multiple of Hkv, d in {64, 128}.  Inputs and outputs do not
- *   overlap.  A position that the table does not hold is reported as
+ *   Hq is a multiple of Hkv, at most 65536, d in {64, 128}.  Inputs and
+ *   outputs do not overlap.  A position that the table does not hold is reported as
  *   FA_ERR_INDEX by fa_get_device_error and its row's values are unspecified.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_MISALIGNED (rows and
  * tables 16 bytes, int arrays 4, the workspace 256), FA_ERR_CUDA.
@@ -395,13 +395,18 @@ fa_status fa_rope_table(float* table, long long rows, int rope_dim,
                         double base, void* stream);
 
 /*
- * fa_qk_norm_rope -- norm and rotation in front of fa_fwd.
+ * fa_qk_norm_rope -- norm and rotation in front of fa_fwd.  With Hkv = Hq the
+ * outputs are what fa_fwd, fa_bwd, fa_fwd_decode and their variants take; those
+ * have one number of heads, so with Hkv < Hq each key and value head has to be
+ * repeated Hq / Hkv times for them, and its gradients summed over the repeats
+ * before fa_qk_norm_rope_bwd.  fa_fwd_paged reads grouped heads as they are.
  *   q [B,N,Hq,d], k and v [B,N,Hkv,d] bf16 with strides[9] = (batch, token,
  *             head) of q, k, v -- for example three parts of one projection.
  *             v (with v_out) may be NULL; it is moved unchanged.
  *   positions [B,N] int32, or NULL: token n has position n (rope_rows >= N).
  *   q_out [B,Hq,N,d], k_out, v_out [B,Hkv,N,d] bf16, contiguous, written.
  * One of the norm and the rotation may be absent, not both.  One launch.
+ * Limits, here and backward: B, N >= 1, B * N <= 2^30.
  */
 fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v,
                           const long long* strides, const void* q_weight,
@@ -450,9 +455,10 @@ fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out,
  * sequence may have none; rows outside seq_start[0] .. seq_start[S]-1 belong
  * to nobody, and nothing is written for them.  Lengths, starts and pages are
  * device memory and are read by the kernels, so a captured graph follows their
- * values.  One that is out of range (or starts that decrease) is reported as
- * FA_ERR_INDEX by fa_get_device_error, and its sequence's rows are unspecified;
- * nothing outside the given buffers is touched.
+ * values.  One that is out of range is reported as FA_ERR_INDEX by
+ * fa_get_device_error, and its sequence's rows are unspecified (where starts
+ * decrease or leave 0 .. T, those of every sequence); nothing outside the given
+ * buffers is touched.
  *
  * fa_paged_append -- writes the new tokens' keys and values behind the rows
  * that a sequence has, with norm and rotation on the way (see above).
@@ -499,7 +505,8 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v,
  * Weights are rounded to bf16 for P V and O is normalised by their sum, as in
  * fa_fwd; scores, statistics and partial results are fp32.  Up to three
  * launches.  Intended for a few new tokens per sequence; any number is right.
- * T = 0 does nothing.  Limits: T * Hq <= 2^24, num_pages * Hkv < 2^31.
+ * T = 0 does nothing.  Limits: T * Hq <= 2^24, num_pages * Hkv < 2^31,
+ * prefix_len and max_pages * page_size <= 2^30.
  */
 size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d,
                                int page_size, int max_pages, int prefix_len,

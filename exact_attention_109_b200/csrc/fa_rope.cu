@@ -16,14 +16,15 @@ using fa_host::aligned;
 
 // CTAs of the backward kernel at most, and so rows of its dw partials in the
 // workspace: two waves of the two that an SM's registers hold, on 148 SMs.
+constexpr int kBwdCtasPerSm = 2;
 constexpr int kMaxBwdCtas = 592;
 constexpr long long kMinHeads = 2;    // heads that a CTA takes at least
 constexpr long long kManyHeads = 16;  // from twice that in one wave on, CTAs take half each:
                                       // the second wave evens out the first (16384 tokens of
                                       // 48 heads of 128: 102 -> 100 us)
-// CTAs up to which the heads of a token block are spread over more CTAs: three
-// on each of 148 SMs, one wave.
-constexpr long long kWantCtas = 444;
+// CTAs of the forward kernel that an SM holds: up to one wave of them, the heads
+// of a token block are spread over more CTAs.
+constexpr int kPrepCtasPerSm = 3;
 constexpr int kHeadsPerCta = 16;
 
 // Strides (in elements) of one input tensor: 16-byte rows, no negative step.
@@ -97,20 +98,20 @@ fa::RopeParams rope_params(const void* wq, const void* wk, int w_f32, float eps,
 // than about 16 heads for one.  16384 tokens of 48 heads of 128: 73 us with all
 // heads in a CTA, 69.5 with 24, 68 with 16 (the last wave is shorter), 77 with
 // 10 (the set-up of a CTA counts).
-int head_groups(long long blocks, int heads) {
+int head_groups(long long blocks, int heads, int sms) {
     const long long g =
-        std::max<long long>(kWantCtas / blocks, heads / kHeadsPerCta);
+        std::max<long long>(1ll * kPrepCtasPerSm * sms / blocks, heads / kHeadsPerCta);
     return static_cast<int>(std::max(1ll, std::min<long long>(g, heads)));
 }
 
 template <int D, bool IL, bool PAGED>
 cudaError_t launch_prep(const fa::HeadRows& q, const fa::HeadRows& k, const fa::HeadRows& v,
                         fa::RopeParams p, const fa::PrepOut& out, const fa::PagedDest& dst,
-                        cudaStream_t s) {
+                        int sms, cudaStream_t s) {
     constexpr int TOKENS = fa::kRopeThreads / (D / 8);
     const long long blocks = (static_cast<long long>(p.B) * p.N + TOKENS - 1) / TOKENS;
     const int heads = p.Hq + p.Hkv + (v.p ? p.Hkv : 0);
-    const int groups = head_groups(blocks, heads);
+    const int groups = head_groups(blocks, heads, sms);
     p.heads_per_cta = (heads + groups - 1) / groups;
     const dim3 grid(static_cast<unsigned>(blocks), (heads + p.heads_per_cta - 1) / p.heads_per_cta);
     return fa_host::launch_overlapped(fa::fa_prep_kernel<D, IL, PAGED>, grid, fa::kRopeThreads, 0,
@@ -120,24 +121,24 @@ cudaError_t launch_prep(const fa::HeadRows& q, const fa::HeadRows& k, const fa::
 template <bool PAGED>
 cudaError_t launch_prep_any(const fa::HeadRows& q, const fa::HeadRows& k, const fa::HeadRows& v,
                             const fa::RopeParams& p, const fa::PrepOut& out,
-                            const fa::PagedDest& dst, int d, int il, cudaStream_t s) {
+                            const fa::PagedDest& dst, int d, int il, int sms, cudaStream_t s) {
     if (d == 64)
-        return il ? launch_prep<64, true, PAGED>(q, k, v, p, out, dst, s)
-                  : launch_prep<64, false, PAGED>(q, k, v, p, out, dst, s);
-    return il ? launch_prep<128, true, PAGED>(q, k, v, p, out, dst, s)
-              : launch_prep<128, false, PAGED>(q, k, v, p, out, dst, s);
+        return il ? launch_prep<64, true, PAGED>(q, k, v, p, out, dst, sms, s)
+                  : launch_prep<64, false, PAGED>(q, k, v, p, out, dst, sms, s);
+    return il ? launch_prep<128, true, PAGED>(q, k, v, p, out, dst, sms, s)
+              : launch_prep<128, false, PAGED>(q, k, v, p, out, dst, sms, s);
 }
 
 template <int D, bool IL>
 cudaError_t launch_prep_bwd(const fa::HeadRows (&dy)[3], const fa::HeadRows (&x)[2],
                             const fa::HeadRowsOut (&dx)[3], fa::RopeParams p, float* part,
-                            float* dwq, float* dwk, cudaStream_t s) {
+                            float* dwq, float* dwk, int sms, cudaStream_t s) {
     constexpr int TOKENS = fa::kRopeThreads / (D / 8);
     const long long blocks = (static_cast<long long>(p.B) * p.N + TOKENS - 1) / TOKENS;
     const int heads = p.Hq + p.Hkv + (dy[2].p ? p.Hkv : 0);
     const long long units = blocks * heads;
-    constexpr int kWave = kMaxBwdCtas / 2;
-    long long per_cta = std::max(kMinHeads, (units + kWave - 1) / kWave);
+    const int wave = std::min(kMaxBwdCtas / 2, kBwdCtasPerSm * sms);
+    long long per_cta = std::max(kMinHeads, (units + wave - 1) / wave);
     if (per_cta >= 2 * kManyHeads) per_cta = (per_cta + 1) / 2;  // still no more than two waves
     const int grid = static_cast<int>((units + per_cta - 1) / per_cta);
     const auto kernel =
@@ -213,7 +214,7 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v, const lon
                              static_cast<__nv_bfloat16*>(v_out)};
     const cudaError_t e = launch_prep_any<false>(
         rows_of(q, strides), rows_of(k, strides + 3), rows_of(v, v ? strides + 6 : none), p, out,
-        fa::PagedDest{}, d, interleaved, static_cast<cudaStream_t>(stream));
+        fa::PagedDest{}, d, interleaved, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -268,13 +269,10 @@ fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void
                                    rows_out(dv, dv ? grad_strides + 6 : none)};
     float* part = static_cast<float*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (d == 64)
-        e = interleaved ? launch_prep_bwd<64, true>(dy, x, dx, p, part, dq_weight, dk_weight, s)
-                        : launch_prep_bwd<64, false>(dy, x, dx, p, part, dq_weight, dk_weight, s);
-    else
-        e = interleaved ? launch_prep_bwd<128, true>(dy, x, dx, p, part, dq_weight, dk_weight, s)
-                        : launch_prep_bwd<128, false>(dy, x, dx, p, part, dq_weight, dk_weight, s);
+    const auto launch =
+        d == 64 ? (interleaved ? launch_prep_bwd<64, true> : launch_prep_bwd<64, false>)
+                : (interleaved ? launch_prep_bwd<128, true> : launch_prep_bwd<128, false>);
+    const cudaError_t e = launch(dy, x, dx, p, part, dq_weight, dk_weight, sms, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -325,7 +323,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, const lon
                     sv[3] = {0, strides[4], strides[5]};
     const cudaError_t e =
         launch_prep_any<true>(rows_of(q, sq), rows_of(k, sk), rows_of(v, sv), p, fa::PrepOut{},
-                              dst, d, interleaved, static_cast<cudaStream_t>(stream));
+                              dst, d, interleaved, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -18,35 +18,38 @@ constexpr int kMaxDevices = 64;
 // CTAs at most: they bound the workspace.
 constexpr long long kMaxPrefixCtas = 512;
 constexpr int kMaxLineCtas = 444;
+// The figures of the rules below: microseconds of GPU time for one call, events
+// around it, L2 flushed before, max_new tight; sequences of one token and 300 own
+// keys unless said otherwise, pages of 64.
+//
 // Query rows of a key head for which the prefix joins the line of the sequences:
-// a row tile of the line, and a launch less.  12 sequences of one token and 300
-// own keys behind 1024 / 4096 / 16384 / 65536 keys, 16 heads of 64: 18.4 / 21.2 /
-// 30.7 / 64.2 us in the line, 22.8 / 25.5 / 35.8 / 70.5 on the tensor-core path;
-// 16 heads of 128: 24.6 / 28.9 / 45.1 / 110.6 and 27.7 / 32.5 / 47.2 / 105.7.  Four
-// query heads a key head (four sequences, 4 heads of 64) gain from the other
-// path at 16384 alone: 22.5 against 18.5.
+// a row tile of the line, and a launch less.  12 sequences behind 1024 / 16384 /
+// 65536 keys, 16 heads of 64: 18 / 31 / 64 in the line, 23 / 35 / 71 on the
+// tensor-core path; 16 heads of 128: 23 / 45 / 110 and 27 / 47 / 105.  32 sequences,
+// 8 heads of 128, behind 1024 / 16384: 25 / 45 in the line, 26 / 38 not.
 constexpr int kLinePrefixRows = 16;
-// Rows of a sequence and key head up to which the line's tiles have 8: 8 rows of
-// 16 sequences of 4096 keys, 4 heads of 128 / 64: 33.9 / 22.6 us, 35.3 / 23.6 in
-// tiles of 16; 12 rows, which read their keys twice in tiles of 8: 53.2 / 29.4
-// and 39.1 / 23.8.
+// Rows of a sequence and key head up to which the line's tiles have 8.  16
+// sequences of 4096 keys without a prefix, 4 heads of 128 / 64: 8 rows 37.5 / 26.6,
+// in tiles of 16 39.1 / 26.7; 12 rows, which read their keys twice in tiles of 8,
+// 56.9 / 32.8, and 42.7 / 27.8 in those of 16.
 constexpr int kSmallTileRows = 8;
 // Keys of a prefix in the line up to which two tiles of 8 rows, the second of
 // which finds the keys in L2, are as good as one of 16 for it and better for the
-// own keys: 16 sequences as above, 16 heads of 128, behind 256 / 1024 / 4096 keys
-// 22.9 / 24.6 / 31.1 us in tiles of 8, 26.6 / 28.7 / 31.6 in tiles of 16; behind
-// 16384 / 65536 keys 68.5 / 196 and 48.2 / 111.  Heads of 64: 18.4 / 20.1 / 22.5
-// and 20.5 / 20.5 / 22.5, 35.5 / 88 and 32.5 / 67.
+// own keys.  16 sequences, 16 heads of 128, behind 256 / 1024 / 4096 keys: 23 / 25 /
+// 31 in tiles of 8, 27 / 29 / 32 in tiles of 16; behind 16384 / 65536 keys 69 / 196
+// and 48 / 111.  Heads of 64: 18 / 20 / 22.5 and 20.5 / 20.5 / 22.5, 36 / 88 and 33 / 67.
 constexpr int kTwoTileKeys = 4096;
 // Query rows of a key head up to which the prefix kernel takes them twice, with
-// heads of 64: 20 rows of 32 heads behind 4096 / 16384 / 65536 keys 31.6 / 50.7 /
-// 123 us, 32.7 / 56.4 / 143 with two idle softmax warps.  Heads of 128 are bound
-// by HBM there (199 us either way) and keep their rows once.
+// heads of 64: 20 sequences, 32 heads, behind 4096 / 16384 / 65536 keys 36 / 54 /
+// 129, 38 / 60 / 148 with two idle softmax warps; 64 sequences behind 16384 75 and
+// 79.  Heads of 128 are bound by HBM there (199 either way) and keep their rows once.
 constexpr int kHalvesRows = 64;
 // Output rows up to which the merge takes four warps for each: few rows may have
-// many pieces, many rows fill the GPU anyway.  32 rows behind 16384 keys: 22 us
-// with four, 34 with one; 16 rows behind 1024: 12.3 and 14.2; 2048 rows with 17
-// pieces each: 73 and 69.
+// many pieces, many rows fill the GPU anyway.  Heads of 128, four warps and one:
+// 16 rows (one sequence of 37 keys) behind 1024 keys 16.4 and 18.0; 32 rows behind
+// 16384 39 and 43; 16 rows of one sequence of 65536 keys 103 and 108; 1024 rows
+// behind 16384 41.6 and 40.8; 2048 behind 16384, 512 own keys, 64 and 61; 4096
+// behind 65536 161 and 154.
 constexpr long long kWideMergeRows = 1024;
 
 struct Plan {

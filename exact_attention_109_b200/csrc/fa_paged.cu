@@ -235,8 +235,10 @@ size_t fa_paged_workspace_size(int S, int T, int Hq, int Hkv, int d, int page_si
     if (check_sizes(S, T, Hq, Hkv, d, page_size, max_pages, prefix_len, max_new) != FA_OK ||
         T == 0)
         return 0;
-    // Enough for any SM count: the splits are bounded by the sizes alone.
-    const Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len, max_new);
+    // Enough for any SM count: the splits are bounded by the sizes alone.  And for
+    // any shorter prefix, which may be cut into small tiles: they make the most CTAs.
+    Plan pl = plan_rows(T, Hq / Hkv, Hkv, d, prefix_len, max_new);
+    pl.tile_rows = 8;
     const int ctas = line_ctas(pl, S, T, Hq / Hkv, Hkv, d, page_size, max_pages, prefix_len,
                                max_new, kMaxLineCtas);
     const size_t slots = prefix_len == 0 ? 0 : 1 + prefix_slots(pl);

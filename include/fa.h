@@ -499,7 +499,9 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v,
  *   o         [T,Hq,d] bf16 and lse [T,Hq] fp32, written.  A row that sees no
  *             key gets O = 0, LSE = -inf.
  *   workspace >= fa_paged_workspace_size(...) bytes, 256-byte aligned,
- *             clobbered; may be NULL when T = 0.
+ *             clobbered; may be NULL when T = 0.  One for the longest prefix
+ *             is enough for the shorter ones; fewer tokens or sequences may
+ *             need more.
  * Query head h reads key head h / (Hq / Hkv).  Cached rows that a token does
  * not see may hold anything, infinities and NaN included, and never reach it.
  * Weights are rounded to bf16 for P V and O is normalised by their sum, as in

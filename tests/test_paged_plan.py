@@ -90,3 +90,14 @@ def test_rows_of_many_partial_results(rows, P, n, d):
         want = torch.logsumexp(c["scale"] * (keys @ q), 0)
         units = (2 * d + 4) * top + 2 * max(chunk, 64 * quota) + 5 * want.abs() + 24 + 3 * parts
         assert abs(lse[t, 0].item() - want.item()) <= ref.U * units.item()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,n,Hq,Hkv", [(9, 1, 1, 1), (16, 1, 2, 2), (2, 8, 1, 1), (4, 1, 6, 2),
+                                        (2, 20, 4, 1), (40, 1, 8, 8)])
+def test_a_workspace_for_a_longer_prefix_is_enough(S, n, Hq, Hkv, d):
+    """A server sizes its workspace for the longest prefix that it holds."""
+    for pages in (1, 3):
+        size = [fa.fa_paged_workspace_size(S, S * n, Hq, Hkv, d, 16, pages, P, n)
+                for P in (0, 1, 64, 700, 2000, 4000, 4096, 4097, 4200, 5000, 8000, 9000, 65536)]
+        assert all(a <= b for a, b in zip(size, size[1:]))

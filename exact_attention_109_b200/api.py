@@ -553,8 +553,11 @@ def _native():
             raise FaError(FA_ERR_UNSUPPORTED, f"{os.path.basename(path)} not built "
                                               "(run __graft_entry__.build())")
         spec = importlib.util.spec_from_file_location(f"{__package__}._fa_binding", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
+        try:
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+        except ImportError as e:
+            raise FaError(FA_ERR_UNSUPPORTED, f"{os.path.basename(path)} does not load: {e}") from e
         module.set_status_error(FaError)
         _binding = module
     return _binding

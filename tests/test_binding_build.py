@@ -37,3 +37,12 @@ def test_another_torch_builds_its_own(other_torch, monkeypatch):
     assert len(ran) == 1 and ran[0][0] == "g++"
     assert ran[0][ran[0].index("-o") + 1] == build.binding_path()
     assert "9.9.9+other" in build.binding_path()
+
+
+def test_a_file_that_does_not_load_is_an_error(monkeypatch, tmp_path):
+    bad = tmp_path / "_fa_binding.so"
+    bad.write_bytes(b"not a library")
+    monkeypatch.setattr(build, "binding_path", lambda: str(bad))
+    monkeypatch.setattr(fa.api, "_binding", None)
+    with pytest.raises(fa.FaError, match="does not load"):
+        fa.paged_append(*[None] * 8)
